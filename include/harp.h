@@ -334,6 +334,169 @@ int harp_stack_uses_fused_step(harp_stack stack, int batch);
 harp_status harp_stack_step(harp_stack stack, int batch, const void* x, harp_dtype xt, void* out,
                             harp_dtype ot, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- serving operators
+ * What stands between the rotated linears of a served model: norms, rotary positions, a
+ * paged key-value cache and the attention that reads it, and the linears that a low-bit
+ * recipe leaves at 8 bits (output head, sensitive layers). Their rows may be strided views:
+ * strides count elements, the innermost dimension is contiguous. Unlike the entry points
+ * above, a pointer only needs the alignment its description gives. They are launched with
+ * programmatic stream serialisation; every kernel waits for the one before it, so the order
+ * of a stream holds as always. Each call can be captured into a CUDA graph after a first
+ * call on the device. */
+
+/* RMS norm with the residual's addition:
+ *   h = x + residual (x without residual),  y = h / sqrt(mean(h^2) + eps) * weight.
+ *   rows >= 0, 1 <= n <= 32768 (wider: HARP_ERR_UNSUPPORTED), eps >= 0.
+ *   x            : device [rows][n], dtype xt, x_stride between rows.
+ *   residual     : device [rows][n], dtype rt, or NULL.   weight: device [n], dtype wt, or NULL (1).
+ *   residual_out : device [rows][n], dtype rt, receives h rounded to rt, or NULL. May equal
+ *                  residual, or x when xt == rt, with the same stride. The norm uses h
+ *                  before that rounding.
+ *   y            : device [rows][n], dtype yt. May equal x when yt == xt, with the same stride.
+ * h and the sums are fp32, the root is fp64. Pointers 16-byte aligned, any strides >= n; rows
+ * on 16-byte boundaries take wide accesses. */
+harp_status harp_rmsnorm(int64_t rows, int64_t n, float eps, const void* x, harp_dtype xt, int64_t x_stride,
+                         const void* residual, harp_dtype rt, int64_t r_stride, const void* weight, harp_dtype wt,
+                         void* residual_out, int64_t ro_stride, void* y, harp_dtype yt, int64_t y_stride, void* stream);
+
+/* The same with an 8-bit output: for every row and block b of 128 columns
+ *   scale[b * scale_ld + row] = s = max |y| / 448 over the block (1 where that is 0),
+ *   q = e4m3(y / s), nearest even, saturating.
+ *   q     : device [rows][n] e4m3, q_stride bytes between rows (a multiple of 16 for
+ *           harp_linear8_fwd).   scale: device fp32 [ceil(n / 128)][scale_ld], scale_ld >= rows
+ *           (a multiple of 4 for harp_linear8_fwd).
+ * A block that holds NaN or infinity dequantizes to NaN throughout. q and scale must not
+ * alias the inputs. */
+harp_status harp_rmsnorm_q8(int64_t rows, int64_t n, float eps, const void* x, harp_dtype xt, int64_t x_stride,
+                            const void* residual, harp_dtype rt, int64_t r_stride, const void* weight, harp_dtype wt,
+                            void* residual_out, int64_t ro_stride, void* q, int64_t q_stride, float* scale,
+                            int64_t scale_ld, void* stream);
+
+/* q and scale of x itself, as harp_rmsnorm_q8 without the norm. */
+harp_status harp_quantize_q8(int64_t rows, int64_t n, const void* x, harp_dtype xt, int64_t x_stride, void* q,
+                             int64_t q_stride, float* scale, int64_t scale_ld, void* stream);
+
+/* e4m3 codes of a weight matrix with a scale per 128 x 128 block:
+ *   s = max |W| / 448 over the block (1 where that is 0), q = e4m3(W / s).
+ *   W : device [n_out][n_in], dtype wt.   q: device [n_out][n_in], q_stride bytes between rows.
+ *   scale : device fp32 [ceil(n_out / 128)][ceil(n_in / 128)]. */
+harp_status harp_quantize_weights_q8(int64_t n_out, int64_t n_in, const void* W, harp_dtype wt, int64_t w_stride, void* q,
+                                     int64_t q_stride, float* scale, void* stream);
+
+/* An 8-bit linear: y[t][n] = sum_b x_scale[b][t] scale[n / 128][b] sum_{k in block b} x[t][k] codes[n][k].
+ *   codes : device e4m3 [n_out][n_in], row_stride bytes between rows (a multiple of 16);
+ *   scale : device fp32 [ceil(n_out / 128)][ceil(n_in / 128)].
+ * Both BORROWED: keep them alive and unchanged until harp_destroy_layer8. Any n_in and n_out
+ * up to 2^22. The handle owns no device memory. */
+typedef struct harp_layer8_s* harp_layer8;
+harp_status harp_create_layer8(harp_layer8* out, int64_t n_in, int64_t n_out, const void* codes, int64_t row_stride,
+                               const float* scale, void* stream);
+harp_status harp_destroy_layer8(harp_layer8 layer);
+
+/* y for `tokens` rows (0..2^24), on the device the layer was created on.
+ *   x       : device e4m3 [tokens][n_in], 16-byte aligned, x_stride a multiple of 16.
+ *   x_scale : device fp32 [ceil(n_in / 128)][scale_ld], 16-byte aligned, scale_ld a multiple
+ *             of 4, at least tokens.
+ *   y       : device [tokens][n_out] of dtype yt, must not alias x.
+ * Products of a block are summed on the tensor cores, their scaled sums in fp32 in a fixed
+ * order: a call repeats its results exactly. Takes no workspace. A device-side wait that runs
+ * out reports HARP_ERR_TIMEOUT (sites 100-107). */
+harp_status harp_linear8_fwd(harp_layer8 layer, int64_t tokens, const void* x, int64_t x_stride, const float* x_scale,
+                             int64_t scale_ld, void* y, harp_dtype yt, int64_t y_stride, void* stream);
+
+/* Rotary frequencies, radians per position, of rot_dim / 2 pairs, into HOST memory:
+ *   NONE   : f_i = base^(-2 i / rot_dim);
+ *   LINEAR : f_i / factor (positions interpolated);
+ *   NTK    : base * factor^(rot_dim / (rot_dim - 2)) in place of base;
+ *   BANDS  : with r_i = original f_i / 2 pi turns in the original length, g = clamp((r_i - low) /
+ *            (high - low), 0, 1): g f_i + (1 - g) f_i / factor;
+ *   RAMP   : the same with g linear in the pair's index, from 1 at the (floored) index whose
+ *            pair makes `high` turns to 0 at the (ceiled) index whose pair makes `low`.
+ * rot_dim even, 2..256; base > 1; factor >= 1; original > 0 and 0 < low < high where used. */
+typedef enum { HARP_ROPE_NONE = 0, HARP_ROPE_LINEAR = 1, HARP_ROPE_NTK = 2, HARP_ROPE_BANDS = 3, HARP_ROPE_RAMP = 4 } harp_rope_scaling;
+harp_status harp_rope_frequencies(int rot_dim, double base, harp_rope_scaling scaling, double factor, double original,
+                                  double low, double high, double* freq);
+
+/* A rotary plan: the first rot_dim of head_dim coordinates turn by pos * freq[i], pairs
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved; cos and sin are multiplied by
+ * amplitude (1, or the attention factor of a stretched context). The other coordinates are
+ * copied. head_dim and rot_dim even, rot_dim <= head_dim <= 256.
+ *   freq : HOST double [rot_dim / 2], finite, magnitude at most 1000 (copied).
+ * The plan owns no device memory and works on every device. Angles are reduced in fp64, so
+ * every int32 position keeps full precision. */
+typedef struct harp_rope_s* harp_rope;
+harp_status harp_rope_create(harp_rope* out, int head_dim, int rot_dim, int interleaved, const double* freq, double amplitude);
+harp_status harp_rope_destroy(harp_rope rope);
+
+/* y = x with every head of token t turned by positions[t] (inverse: by -positions[t], which
+ * is also the gradient of the forward call). Rows of negative positions are left as they were.
+ *   x, y : device [tokens][heads][head_dim] of dtypes xt / yt, aligned to their type; y may
+ *          equal x with equal dtypes and strides.   positions: device int32 [tokens]. */
+harp_status harp_rope_apply(harp_rope rope, int64_t tokens, int heads, const int32_t* positions, const void* x, harp_dtype xt,
+                            int64_t x_token_stride, int64_t x_head_stride, void* y, harp_dtype yt, int64_t y_token_stride,
+                            int64_t y_head_stride, int inverse, void* stream);
+
+/* A paged key-value cache (one layer): row r of page p of key head h starts at element
+ * p * page_stride + h * head_stride + r * row_stride of k and of v. Position j of sequence s
+ * lies in page page_table[s * max_pages + j / page_size], row j % page_size.
+ * dtype bf16 or f16; page_size a power of two, at most 4096; head_dim even, at most 256; strides
+ * multiples of 8; k and v 16-byte aligned. Page indices outside [0, n_pages) are never
+ * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93). */
+typedef struct {
+  void* k;
+  void* v;
+  harp_dtype dtype;
+  int n_kv_heads, head_dim, page_size;
+  int64_t n_pages, page_stride, head_stride, row_stride;
+} harp_kv_cache;
+
+/* One launch: q_out = turned q, and the cache rows of every token's position = (turned k, v).
+ * Token t belongs to sequence seq_ids[t] (NULL: t). Tokens of negative positions write
+ * nothing. A token whose sequence or page is out of range writes no cache row and is
+ * reported. No two tokens of a call may share a sequence and a position.
+ *   q : device [tokens][n_heads][head_dim], k, v: [tokens][n_kv_heads][head_dim], dtype xt.
+ *   q_out : dtype yt; may equal q with equal dtypes and strides.
+ *   page_table : device int32 [n_seqs][max_pages]. */
+harp_status harp_rope_append(harp_rope rope, const harp_kv_cache* cache, int64_t tokens, int n_heads, const int32_t* positions,
+                             const int32_t* seq_ids, int n_seqs, const int32_t* page_table, int64_t max_pages, const void* q,
+                             int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, harp_dtype xt,
+                             void* q_out, harp_dtype yt, int64_t o_token_stride, int64_t o_head_stride, void* stream);
+
+/* Attention of one new token per sequence over the cache:
+ *   out_h = sum_j p_j v_j, p = softmax_j(scale q_h . k_j), j in [max(0, len - window), len),
+ *   len = seq_lens[s] (the new token's own row included); window 0: all of them.
+ * Query head h reads key head h / (n_heads / n_kv_heads). A sequence of length 0 gets zeros
+ * and lse -infinity; rows of negative length are left as they were; a length beyond
+ * max_pages * page_size is cut to it and reported. Rows outside the mask are not read.
+ *   q, out : device [n_seqs][n_heads][head_dim] of the cache's dtype, rows on 4-byte boundaries.
+ *   lse    : device fp32 [n_seqs][n_heads], log sum exp of the scaled scores, or NULL.
+ *   n_seqs <= 65535; head_dim 32, 64, 96, 128, 192 or 256 (else HARP_ERR_UNSUPPORTED).
+ *   workspace : device, 256-byte aligned, harp_paged_attention_workspace_size bytes; overwritten,
+ *               needs no initial contents. Calls that may overlap need workspaces of their own.
+ * The lengths are read on the device; a captured call follows them as they grow. */
+harp_status harp_paged_attention_workspace_size(int head_dim, size_t* bytes);
+harp_status harp_paged_attention(const harp_kv_cache* cache, int n_seqs, int n_heads, const void* q, int64_t q_seq_stride,
+                                 int64_t q_head_stride, const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens,
+                                 float scale, int window, void* out, int64_t o_seq_stride, int64_t o_head_stride, float* lse,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/* One decode step of a stack over a real cache: as harp_stack_step, with the one-key
+ * attention replaced by rotary positions and attention over the cache. Row b is sequence b's
+ * new token at positions[b] (device int32 [batch]); its key and value are written to the cache
+ * first, and it attends to positions 0..positions[b]. Rows of negative positions touch no
+ * cache and take attention 0.
+ *   cache : the first block's cache; block l's k and v start l * layer_stride elements further.
+ *           n_kv_heads and head_dim as the stack's; head_dim as harp_paged_attention needs.
+ *   x, out : as for harp_stack_step (batch 1..256). workspace: 256-byte aligned,
+ *           harp_stack_cached_workspace_size bytes. window as for harp_paged_attention.
+ * Takes the per-linear path at every batch. */
+harp_status harp_stack_cached_workspace_size(harp_stack stack, int batch, size_t* bytes);
+harp_status harp_stack_step_cached(harp_stack stack, int batch, const void* x, harp_dtype xt, void* out, harp_dtype ot,
+                                   harp_rope rope, const harp_kv_cache* cache, int64_t layer_stride, const int32_t* positions,
+                                   const int32_t* page_table, int64_t max_pages, int window, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

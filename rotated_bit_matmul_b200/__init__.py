@@ -20,7 +20,21 @@ from ._lib import (HARP_BF16, HARP_F16, HARP_F32, HarpError, call, load)  # noqa
 
 __all__ = ["HarpError", "harp_butterfly_fwd", "harp_butterfly_inv", "harp_quantize_weights", "HarpLayer",
            "HarpStack", "HarpMixedRadix", "rotate_weights_device", "harp_quantize_angles", "harp_calib_fit", "harp_device_status",
-           "harp_test_set_faults", "load"]
+           "harp_test_set_faults", "load", "harp_rmsnorm", "harp_rmsnorm_q8", "harp_quantize_q8", "harp_quantize_weights_q8",
+           "HarpLinear8", "HarpCache", "HarpRope", "harp_paged_attention"]
+
+_SERVING = ("harp_rmsnorm", "harp_rmsnorm_q8", "harp_quantize_q8", "harp_quantize_weights_q8", "HarpLinear8", "HarpCache",
+            "HarpRope", "harp_paged_attention", "harp_paged_attention_workspace_bytes")
+
+
+def __getattr__(name):
+    """The serving operators, bound on first use (their module imports torch)."""
+    if name not in _SERVING:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import serving
+    for n in _SERVING:
+        globals()[n] = getattr(serving, n)
+    return globals()[name]
 
 
 def _torch():
@@ -330,6 +344,36 @@ class HarpStack:
         ws = workspace if workspace is not None else self.workspace(x2.shape[0])
         call("harp_stack_step", self.handle, x2.shape[0], _p(x2), _dt(x2), _p(out), _dt(out), _p(ws), ws.numel(),
              _stream())
+        return out
+
+    def cached_workspace(self, batch: int):
+        """A workspace for step_cached (fresh; steps that may overlap need one each)."""
+        n = ctypes.c_size_t()
+        call("harp_stack_cached_workspace_size", self.handle, int(batch), ctypes.byref(n))
+        return _torch().empty(n.value, dtype=_torch().uint8, device=self.device)
+
+    def step_cached(self, x, rope, cache, positions, page_table, window=0, out_dtype=None, out=None, workspace=None):
+        """One decode step over a real cache (wraps harp_stack_step_cached): row b of x is sequence
+        b's new token at positions[b]; its keys and values are appended to the cache (HarpCache
+        with one layer per block) and every head attends to positions 0..positions[b]."""
+        torch = _torch()
+        _need_cuda(x, positions, page_table, cache.k, out, workspace)
+        x2 = x.reshape(-1, self.hidden).contiguous()
+        batch = x2.shape[0]
+        if cache.n_layers != len(self.layers) // 7:
+            raise ValueError(f"the cache has {cache.n_layers} layers, the stack {len(self.layers) // 7} blocks")
+        if positions.dtype != torch.int32 or positions.shape != (batch,) or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous int32 [{batch}]")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch or \
+                not page_table.is_contiguous():
+            raise ValueError(f"page_table must be contiguous int32 [{batch}, pages]")
+        if out is None:
+            out = torch.empty(x2.shape, dtype=out_dtype or torch.float32, device=x.device)
+        ws = workspace if workspace is not None else self.cached_workspace(batch)
+        with torch.cuda.device(x.device):
+            call("harp_stack_step_cached", self.handle, batch, _p(x2), _dt(x2), _p(out), _dt(out), rope.handle,
+                 cache.layer(0), cache.layer_stride, _p(positions), _p(page_table), page_table.shape[1], int(window),
+                 _p(ws), ws.numel(), _stream())
         return out
 
     def close(self):

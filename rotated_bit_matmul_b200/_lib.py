@@ -24,6 +24,8 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
+_D = ctypes.c_double
 SIGNATURES = {
     "harp_last_error": (ctypes.c_char_p, []),
     "harp_device_status": (_I, [_P]),
@@ -52,7 +54,31 @@ SIGNATURES = {
     "harp_calib_workspace_size": (_I, [_I64, _I64, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "harp_calib_fit": (_I, [_I64, _I64, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_double, _P, _P, _P, _P,
                             _SZ, _P]),
+    "harp_rmsnorm": (_I, [_I64, _I64, _F, _P, _I, _I64, _P, _I, _I64, _P, _I, _P, _I64, _P, _I, _I64, _P]),
+    "harp_rmsnorm_q8": (_I, [_I64, _I64, _F, _P, _I, _I64, _P, _I, _I64, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "harp_quantize_q8": (_I, [_I64, _I64, _P, _I, _I64, _P, _I64, _P, _I64, _P]),
+    "harp_quantize_weights_q8": (_I, [_I64, _I64, _P, _I, _I64, _P, _I64, _P, _P]),
+    "harp_create_layer8": (_I, [ctypes.POINTER(_P), _I64, _I64, _P, _I64, _P, _P]),
+    "harp_destroy_layer8": (_I, [_P]),
+    "harp_linear8_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I, _I64, _P]),
+    "harp_rope_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(_D)]),
+    "harp_rope_create": (_I, [ctypes.POINTER(_P), _I, _I, _I, ctypes.POINTER(_D), _D]),
+    "harp_rope_destroy": (_I, [_P]),
+    "harp_rope_apply": (_I, [_P, _I64, _I, _P, _P, _I, _I64, _I64, _P, _I, _I64, _I64, _I, _P]),
+    "harp_rope_append": (_I, [_P, _P, _I64, _I, _P, _P, _I, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
+                              _I, _P, _I, _I64, _I64, _P]),
+    "harp_paged_attention_workspace_size": (_I, [_I, ctypes.POINTER(_SZ)]),
+    "harp_paged_attention": (_I, [_P, _I, _I, _P, _I64, _I64, _P, _I64, _P, _F, _I, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "harp_stack_cached_workspace_size": (_I, [_P, _I, ctypes.POINTER(_SZ)]),
+    "harp_stack_step_cached": (_I, [_P, _I, _P, _I, _P, _I, _P, _P, _I64, _P, _P, _I64, _I, _P, _SZ, _P]),
 }
+
+
+class KVCache(ctypes.Structure):
+    """harp_kv_cache of include/harp.h."""
+
+    _fields_ = [("k", _P), ("v", _P), ("dtype", _I), ("n_kv_heads", _I), ("head_dim", _I), ("page_size", _I),
+                ("n_pages", _I64), ("page_stride", _I64), ("head_stride", _I64), ("row_stride", _I64)]
 
 
 class HarpError(RuntimeError):

@@ -1,0 +1,521 @@
+// Matrix product in e4m3 with a scale for each block of 128.
+//
+//   y[t][n] = sum_b sx[b][t] sw[n / 128][b] * sum_{k in block b} x8[t][k] w8[n][k]
+//
+// Tensor-core kernel. A tile is 128 weight rows (the MMA's M, one row block of sw) by BT
+// tokens (its N); a K step is one block of 128 columns. Warp 0 streams both operands with TMA
+// (no multicast) into a ring of 128-byte-swizzled stages, one lane of warp 1 issues
+// tcgen05.mma kind::f8f6f4 (K = 32 each) into tensor memory, and eight warps read every
+// finished block with tcgen05.ld and add it, times its scales, to fp32 sums in registers.
+// Each K step starts a fresh accumulator: its columns have a scale of their own, so the tensor
+// core never holds a sum over more than 128 products, and several accumulators in tensor
+// memory let the MMAs run ahead of the eight warps.
+//
+// The weights are the M side at every batch: one token needs a 128 x 16 tile, in which only
+// the weights' bytes count, and a thread then owns one weight row, so that a warp's store of
+// one token covers 32 consecutive outputs.
+//
+// Few tokens: the weights' bandwidth bounds the work. The K blocks of a tile are cut over a
+// cluster of up to 8 CTAs; each leaves its fp32 tile in its idle ring, and the cluster adds
+// them in rank order through distributed shared memory (no workspace, no atomics).
+// Many tokens: CTAs are persistent and take tiles in an order that keeps the token tiles of
+// one weight tile together in L2.
+#include "serve.cuh"
+#include "serve.h"
+
+#include <algorithm>
+#include <new>
+
+namespace harp {
+namespace l8 {
+namespace {
+
+constexpr int kBM = 128;        // weight rows of a tile
+constexpr int kBK = 128;        // columns of a K step = columns that share a scale
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 64 + 32 * kSumWarps;
+constexpr int kMaxStages = 12;
+constexpr int kMaxAcc = 8;
+constexpr int kMaxSlots = 32;
+
+// ------------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// K-major operand, 128-byte swizzle, rows of 128 bytes, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3fffu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f8f6f4: fp32 accumulator, A = B = e4m3 (format 0), both K-major
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {  // whole warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {  // whole warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// two fp32 at once: acc + v * (a * b)
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_peer(const float* local, uint32_t cta) {
+  uint32_t ra;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(cta));
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+  return v;
+}
+
+struct Params {
+  CUtensorMap tm_w, tm_x;  // e4m3 rows as bytes, boxes of 128 columns x 128 (BT) rows, 128-byte swizzle
+  int n_out, tokens, kblocks, ntiles, ttiles, stages, splits;
+  const float* sx;         // [kblocks][sx_ld]
+  int64_t sx_ld;
+  const float* sw;         // [ntiles][kblocks]
+  void* y;
+  int yt;
+  int64_t ys;
+  int* status;
+  uint64_t wait_ns;
+};
+
+template <int BT>
+struct Cfg {
+  static constexpr int kStage = kBM * kBK + BT * kBK;
+  static constexpr int kAcc = BT >= 256 ? 2 : BT >= 128 ? 4 : kMaxAcc;
+  // ring of token scales, one slot per K step: at least stages + accumulators (see the producer)
+  static constexpr int kSlots = BT >= 256 ? 8 : BT >= 128 ? 16 : 32;
+  static constexpr int kCols = kAcc * BT;  // tensor-memory columns: a power of two, at least 32
+  static constexpr int kFixed = kSlots * BT * 4 + 1024 /* barriers */ + 1024 /* alignment */;
+};
+
+// Barrier layout (uint64 each) in the 1024 bytes behind the scale ring.
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t accfull[kMaxAcc], accempty[kMaxAcc];
+  uint64_t scale[kMaxSlots];
+  uint32_t tslot;
+};
+static_assert(sizeof(Bars) <= 1024, "barriers");
+
+// tile i of the launch: token tiles of 8 consecutive weight tiles together, so that a wave of
+// CTAs reads few distinct operand tiles
+__device__ __forceinline__ void tile_at(const Params& p, int i, int& nt, int& tt) {
+  constexpr int kGroup = 8;
+  const int per = kGroup * p.ttiles, g = i / per, in = i - g * per;
+  const int wide = min(kGroup, p.ntiles - g * kGroup);
+  tt = in / wide;
+  nt = g * kGroup + in - tt * wide;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(kThreads, 1) linear8_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<BT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int ST = p.stages;
+  constexpr int SL = C::kSlots;
+  float* scale_s = reinterpret_cast<float*>(ring + (size_t)ST * C::kStage);  // [SL][BT]
+  Bars* bars = reinterpret_cast<Bars*>(scale_s + SL * BT);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.y;
+  const int kb0 = (int)((int64_t)split * p.kblocks / p.splits), kb1 = (int)((int64_t)(split + 1) * p.kblocks / p.splits);
+  const int nkb = kb1 - kb0;
+  const int tiles = p.ntiles * p.ttiles;
+
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < C::kAcc; ++i) {
+      mbar_init(&bars->accfull[i], 1);
+      mbar_init(&bars->accempty[i], kSumWarps);
+    }
+    for (int i = 0; i < SL; ++i) mbar_init(&bars->scale[i], 1);
+    fence_mbar_init();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(&bars->tslot, C::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tslot;
+  grid_wait();
+
+  if (warp == 0) {
+    // ---------------- producer
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tm_w);
+      tma_prefetch_desc(&p.tm_x);
+      int k = 0;  // K steps of this CTA so far, over all its tiles
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+        int nt, tt;
+        tile_at(p, i, nt, tt);
+        const uint32_t sbytes = (uint32_t)(min(BT, (p.tokens - tt * BT + 3) & ~3) * 4);
+        for (int kb = kb0; kb < kb1; ++kb, ++k) {
+          const int slot = k % ST;
+          if (k >= ST && !mbar_wait_sleep(&bars->empty[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + (size_t)slot * C::kStage;
+          mbar_arrive_expect_tx(&bars->full[slot], C::kStage);
+          tma_load_2d(st, &p.tm_w, &bars->full[slot], kb * kBK, nt * kBM);
+          tma_load_2d(st + kBM * kBK, &p.tm_x, &bars->full[slot], kb * kBK, tt * BT);
+          // The slot of the scale ring was last read for K step k - SL <= k - ST - kAcc. The
+          // MMA of step k - ST, which has completed, was only issued once the eight warps had
+          // released the accumulator, and with it the scales, of step k - ST - kAcc.
+          uint64_t* sb = &bars->scale[k % SL];
+          mbar_arrive_expect_tx(sb, sbytes);
+          bulk_g2s(scale_s + (k % SL) * BT, p.sx + (int64_t)kb * p.sx_ld + (int64_t)tt * BT, sbytes, sb);
+        }
+      }
+      // copies still in flight land before the CTA may leave
+      for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->full[q % ST], (q / ST) & 1, p.status, 101, p.wait_ns);
+      for (int q = max(0, k - SL); q < k; ++q)
+        mbar_wait(&bars->scale[q % SL], (q / SL) & 1, p.status, 102, p.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = idesc_e4m3(kBM, BT);
+      int k = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int slot = k % ST, b = k % C::kAcc;
+          if (k >= C::kAcc && !mbar_wait_sleep(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns)) ok = false;
+          if (ok && !mbar_wait_sleep(&bars->full[slot], (k / ST) & 1, p.status, 104, p.wait_ns)) ok = false;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + (size_t)slot * C::kStage), x = a + kBM * kBK;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_e4m3(tmem + b * BT, sw128_desc(a + 32 * kk), sw128_desc(x + 32 * kk), idesc, kk != 0);
+          mma_commit(&bars->empty[slot]);
+          mma_commit(&bars->accfull[b]);
+        }
+      // the MMAs in flight end before tensor memory is freed
+      for (int q = max(0, k - C::kAcc); q < k; ++q)
+        mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- scaled sums: thread = weight row, half the tile's tokens
+    constexpr int HC = BT / 2, CH = HC < 32 ? 8 : 32;  // columns per thread, per tcgen05.ld
+    const int quad = warp & 3, c0 = (warp >= 6 ? HC : 0);
+    const int m = quad * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + c0;
+    int k = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      int nt, tt;
+      tile_at(p, i, nt, tt);
+      uint64_t acc[HC / 2];
+#pragma unroll
+      for (int j = 0; j < HC / 2; ++j) acc[j] = 0ull;
+      float sw_l = 0.f;  // lane j: weight scale of K step 32 * (kb / 32) + j
+      for (int kb = 0; kb < nkb; ++kb, ++k) {
+        if ((kb & 31) == 0) sw_l = kb + lane < nkb ? __ldg(p.sw + (int64_t)nt * p.kblocks + kb0 + kb + lane) : 0.f;
+        const float sw = __shfl_sync(0xffffffffu, sw_l, kb & 31);
+        const int b = k % C::kAcc;
+        int got = 1;
+        if (lane == 0)
+          got = mbar_wait_sleep(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
+                mbar_wait_sleep(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
+        if (!__shfl_sync(0xffffffffu, got, 0)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float* sc = scale_s + (k % SL) * BT + c0;
+        const uint64_t sw2 = f32x2(sw, sw);
+#pragma unroll
+        for (int q = 0; q < HC; q += CH) {
+          uint32_t r[CH];
+          if (CH == 8) tmem_ld8(tl + b * BT + q, r);
+          else tmem_ld32(tl + b * BT + q, r);
+          tmem_wait();
+#pragma unroll
+          for (int j = 0; j < CH; j += 4) {
+            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(sc + q + j);
+            acc[(q + j) / 2] = fma2((uint64_t)r[j] | ((uint64_t)r[j + 1] << 32), mul2(s4.x, sw2), acc[(q + j) / 2]);
+            acc[(q + j) / 2 + 1] =
+                fma2((uint64_t)r[j + 2] | ((uint64_t)r[j + 3] << 32), mul2(s4.y, sw2), acc[(q + j) / 2 + 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->accempty[b]);
+      }
+      if (p.splits > 1) {
+        // this CTA's only tile: its ring is idle once every K step has been summed
+        float* part = reinterpret_cast<float*>(ring);  // [BT][128]
+#pragma unroll
+        for (int j = 0; j < HC / 2; ++j) {
+          part[(c0 + 2 * j) * kBM + m] = __uint_as_float((uint32_t)acc[j]);
+          part[(c0 + 2 * j + 1) * kBM + m] = __uint_as_float((uint32_t)(acc[j] >> 32));
+        }
+      } else {
+        const int n = nt * kBM + m;
+        const int64_t t0 = (int64_t)tt * BT + c0;
+        if (n < p.n_out && ok) {
+          const int valid = (int)min((int64_t)HC, p.tokens - t0);
+          auto column = [&](int j) { return __uint_as_float((uint32_t)(j & 1 ? acc[j / 2] >> 32 : acc[j / 2])); };
+          if (p.yt == DT_F32) {
+            float* y = static_cast<float*>(p.y) + t0 * p.ys + n;
+#pragma unroll
+            for (int j = 0; j < HC; ++j)
+              if (j < valid) y[j * p.ys] = column(j);
+          } else {
+            uint16_t* y = static_cast<uint16_t*>(p.y) + t0 * p.ys + n;
+#pragma unroll
+            for (int j = 0; j < HC; j += 2) {
+              const uint32_t v = pack2(column(j), column(j + 1), p.yt);
+              if (j < valid) y[j * p.ys] = (uint16_t)v;
+              if (j + 1 < valid) y[(j + 1) * p.ys] = (uint16_t)(v >> 16);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+  if (p.splits > 1) {
+    cluster_sync_all();  // every partial tile of the cluster is written
+    int nt, tt;
+    tile_at(p, blockIdx.x, nt, tt);
+    const float* part = reinterpret_cast<const float*>(ring);
+    const int valid = min(BT, p.tokens - tt * BT);
+    // this CTA's share of the tile's (token, row) places, 32 rows at a time per warp
+    for (int i = split * (kThreads / 32) + warp; i < valid * (kBM / 32); i += p.splits * (kThreads / 32)) {
+      const int t = i / (kBM / 32), m = (i % (kBM / 32)) * 32 + lane, n = nt * kBM + m;
+      float v = 0.f;
+      for (int s = 0; s < p.splits; ++s) v += ld_peer(part + t * kBM + m, (uint32_t)s);
+      if (n < p.n_out) store_act(p.y, ((int64_t)tt * BT + t) * p.ys + n, p.yt, v);
+    }
+    cluster_sync_all();  // no tile leaves while a peer may still read it
+  }
+  grid_release();
+}
+
+struct Plan {
+  int bt, splits;
+};
+
+// Tile width and K split. Few tokens: the narrowest tile that holds them (fewer bytes of
+// scales and operand per stage), cut so that about one CTA per SM streams weights, each over
+// at least 4 K steps. More: the width with the least (waves x width), the wider on a tie.
+Plan choose(int64_t tokens, int64_t n_out, int kblocks) {
+  const int64_t nt = (n_out + kBM - 1) / kBM;
+  Plan best{256, 1};
+  for (int bt : {16, 32, 64, 128})
+    if (tokens <= bt) {
+      best.bt = bt;
+      break;
+    }
+  if (tokens > 128) {
+    int64_t cost = INT64_MAX;
+    for (int bt : {256, 128, 64}) {
+      const int64_t tiles = nt * ((tokens + bt - 1) / bt), waves = (tiles + 147) / 148;
+      if (waves * bt < cost) {
+        cost = waves * bt;
+        best.bt = bt;
+      }
+    }
+  }
+  const int64_t tiles = nt * ((tokens + best.bt - 1) / best.bt);
+  if (best.bt <= 64)
+    while (best.splits < 8 && tiles * best.splits * 2 <= 160 && kblocks / (best.splits * 2) >= 4) best.splits *= 2;
+  return best;
+}
+
+template <int BT>
+cudaError_t launch_t(Params& p, cudaStream_t st) {
+  using C = Cfg<BT>;
+  int dev = 0, optin = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  static bool attr_done[64] = {false};  // per device
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(linear8_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  const int nkb = (p.kblocks + p.splits - 1) / p.splits;
+  p.stages = std::min(kMaxStages, (optin - C::kFixed) / C::kStage);
+  if (p.splits == 1 && p.ntiles * p.ttiles <= 148) p.stages = std::min(p.stages, std::max(nkb, 2));
+  int smem = C::kFixed + p.stages * C::kStage;
+  // one CTA per SM: two would not fit tensor memory at the widest tiles
+  smem = std::max(smem, 116 * 1024);
+  const int tiles = p.ntiles * p.ttiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = p.splits > 1 ? dim3((unsigned)tiles, (unsigned)p.splits) : dim3((unsigned)std::min(tiles, 148));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = (unsigned)p.splits;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear8_kernel<BT>, p);
+}
+
+}  // namespace
+}  // namespace l8
+}  // namespace harp
+
+using namespace harp;
+
+struct harp_layer8_s {
+  CUtensorMap tm_w;
+  int64_t n_out, n_in;
+  const float* sw;
+  int device;
+};
+
+extern "C" {
+
+harp_status harp_create_layer8(harp_layer8* out, int64_t n_in, int64_t n_out, const void* codes, int64_t row_stride,
+                               const float* scale, void* stream) {
+  (void)stream;
+  if (!out) return set_error(HARP_ERR_INVALID_ARG, "create_layer8: null pointer");
+  *out = nullptr;
+  if (n_in < 1 || n_out < 1 || n_in > (1 << 22) || n_out > (1 << 22))
+    return set_error(HARP_ERR_INVALID_ARG, "create_layer8: n_in=%lld n_out=%lld out of range", (long long)n_in, (long long)n_out);
+  if (!codes || !scale || !aligned_to(codes, 16) || !aligned_to(scale, 16))
+    return set_error(HARP_ERR_INVALID_ARG, "create_layer8: codes and scale must be 16-byte aligned device pointers");
+  if (row_stride < n_in || row_stride % 16)
+    return set_error(HARP_ERR_INVALID_ARG, "create_layer8: row_stride must be a multiple of 16, at least n_in");
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return set_error(HARP_ERR_CUDA, "create_layer8: no CUDA device");
+  harp_layer8_s* L = new (std::nothrow) harp_layer8_s();
+  if (!L) return set_error(HARP_ERR_INVALID_ARG, "create_layer8: out of host memory");
+  L->n_in = n_in;
+  L->n_out = n_out;
+  L->sw = scale;
+  L->device = dev;
+  if (!encode_map_2d(&L->tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, (uint64_t)n_in, (uint64_t)n_out, (uint64_t)row_stride,
+                     l8::kBK, l8::kBM, CU_TENSOR_MAP_SWIZZLE_128B)) {
+    delete L;
+    return set_error(HARP_ERR_CUDA, "create_layer8: cuTensorMapEncodeTiled failed");
+  }
+  *out = L;
+  return HARP_OK;
+}
+
+harp_status harp_destroy_layer8(harp_layer8 layer) {
+  delete layer;
+  return HARP_OK;
+}
+
+harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64_t x_stride, const float* x_scale,
+                             int64_t scale_ld, void* y, harp_dtype yt, int64_t y_stride, void* stream) {
+  if (!L || !x || !x_scale || !y) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: null pointer");
+  if (tokens < 0 || tokens > (1 << 24)) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: tokens=%lld out of range", (long long)tokens);
+  if (!known_dtype(yt)) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: unknown dtype");
+  if (!aligned_to(x, 16) || !aligned_to(x_scale, 16) || !aligned_to(y, dtype_bytes(yt)))
+    return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: x and x_scale must be 16-byte aligned, y aligned to its type");
+  if (x_stride < L->n_in || x_stride % 16) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: x_stride must be a multiple of 16, at least n_in");
+  if (scale_ld < tokens || scale_ld % 4) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: scale_ld must be a multiple of 4, at least tokens");
+  if (y_stride < L->n_out) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: y_stride is below n_out");
+  if (tokens == 0) return HARP_OK;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return set_error(HARP_ERR_CUDA, "linear8_fwd: no CUDA device");
+  if (dev != L->device) return set_error(HARP_ERR_INVALID_ARG, "linear8_fwd: the layer lives on device %d, the current device is %d", L->device, dev);
+  l8::Params p{};
+  harp_status s = device_status_for_kernels(&p.status);
+  if (s != HARP_OK) return s;
+  p.tm_w = L->tm_w;
+  p.n_out = (int)L->n_out;
+  p.tokens = (int)tokens;
+  p.kblocks = (int)((L->n_in + l8::kBK - 1) / l8::kBK);
+  p.ntiles = (int)((L->n_out + l8::kBM - 1) / l8::kBM);
+  const l8::Plan plan = l8::choose(tokens, L->n_out, p.kblocks);
+  p.ttiles = (int)((tokens + plan.bt - 1) / plan.bt);
+  p.splits = plan.splits;
+  p.sx = x_scale;
+  p.sx_ld = scale_ld;
+  p.sw = L->sw;
+  p.y = y;
+  p.yt = yt;
+  p.ys = y_stride;
+  p.wait_ns = test_hooks().wait_ns;
+  if (!encode_map_2d(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)L->n_in, (uint64_t)tokens, (uint64_t)x_stride,
+                     l8::kBK, (uint32_t)plan.bt, CU_TENSOR_MAP_SWIZZLE_128B))
+    return set_error(HARP_ERR_CUDA, "linear8_fwd: cuTensorMapEncodeTiled failed");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (plan.bt) {
+    case 16: e = l8::launch_t<16>(p, st); break;
+    case 32: e = l8::launch_t<32>(p, st); break;
+    case 64: e = l8::launch_t<64>(p, st); break;
+    case 128: e = l8::launch_t<128>(p, st); break;
+    case 256: e = l8::launch_t<256>(p, st); break;
+  }
+  return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "linear8 launch: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

@@ -1,0 +1,447 @@
+// RMS norm with the residual's addition, and 8-bit quantization with a scale per row and
+// 128 columns.
+//
+//   h = x + r,   y = h / sqrt(mean(h^2) + eps) * w,
+//   8-bit output: s = max |y| / 448 over 128 columns (1 where that is 0), q = e4m3(y / s).
+//
+// One pass: a row's values are loaded once and stay in registers between the sum of squares
+// and the output, so the kernel moves what the formula needs and no more. The sum of squares
+// is fp32 (a thread's few values, then a fixed tree), the mean and its root are taken in
+// fp64 (once per row), and q is an IEEE division, so that a code differs from the exact one
+// only where y / s lies within fp32 rounding of the border between two codes.
+//
+// Two mappings of a row onto threads:
+//   * rows that start on 16-byte boundaries: a thread holds 8 consecutive columns per step
+//     (16-byte loads), 16 lanes share a block of 128;
+//   * other rows (odd widths, strided views): a warp takes a block of 128, lane l its columns
+//     l, l + 32, l + 64, l + 96, so that 2- and 4-byte loads still coalesce.
+#include "serve.cuh"
+
+#include <cuda_fp8.h>
+
+namespace harp {
+namespace {
+
+constexpr int kBlk = 128;        // columns that share a scale
+constexpr int kMaxCols = 32768;  // 1024 threads x 8 columns x 4 steps
+
+struct NormParams {
+  int64_t rows;
+  int n;
+  int norm;  // 0: quantize x as it is
+  float eps;
+  const void* x;
+  int xt;
+  int64_t xs;
+  const void* r;  // residual or null
+  int rt;
+  int64_t rs;
+  const void* w;  // weight or null
+  int wt;
+  void* h;        // residual_out or null (dtype rt)
+  int64_t hs;
+  void* y;        // plain output, or e4m3 codes
+  int yt;
+  int64_t ys;
+  float* scale;   // [blocks][scale_ld]
+  int64_t scale_ld;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float block_scale(float amax) {
+  const float s = amax / 448.f;
+  return s == 0.f ? 1.f : s;
+}
+
+// sum over the blockDim.x threads of this row (a fixed tree, the same in every thread)
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  float t = lane < warps ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+__device__ __forceinline__ float inv_rms(float sum, int n, float eps) {
+  return (float)(1.0 / sqrt((double)sum / n + (double)eps));
+}
+
+// blockDim = (threads per row, rows per CTA); more than one row per CTA only with 32 threads
+template <int STEPS, bool Q8>
+__global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[32];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int tx = threadIdx.x, T = blockDim.x;
+  grid_wait();
+  if (row >= p.rows) return;  // whole warps: a row has at least one
+  const int n = p.n;
+  const int64_t xo = row * p.xs, ro = row * p.rs;
+  float v[STEPS][8];
+  {
+    Raw8 rx[STEPS], rr[STEPS];
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const int c = (k * T + tx) * 8;
+      if (c + 8 <= n) {
+        rx[k] = raw_load8(p.x, xo + c, p.xt);
+        if (p.r) rr[k] = raw_load8(p.r, ro + c, p.rt);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const int c = (k * T + tx) * 8;
+      if (c + 8 <= n) {
+        raw_unpack8(rx[k], p.xt, v[k]);
+        if (p.r) {
+          float t[8];
+          raw_unpack8(rr[k], p.rt, t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][i] += t[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[k][i] = 0.f;
+          if (c + i < n) v[k][i] = load_act(p.x, xo + c + i, p.xt) + (p.r ? load_act(p.r, ro + c + i, p.rt) : 0.f);
+        }
+      }
+    }
+  }
+  if (p.h) {
+    const int64_t ho = row * p.hs;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const int c = (k * T + tx) * 8;
+      if (c + 8 <= n) store8(p.h, ho + c, p.rt, v[k]);
+      else
+        for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.h, ho + c + i, p.rt, v[k][i]);
+    }
+  }
+  if (p.norm) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(v[k][i], v[k][i], s);
+    const float inv = inv_rms(row_sum(s, red), n, p.eps);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const int c = (k * T + tx) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] *= inv;
+      if (p.w) {
+        if (c + 8 <= n) {
+          float t[8];
+          raw_unpack8(raw_load8(p.w, c, p.wt), p.wt, t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][i] *= t[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < n) v[k][i] *= load_act(p.w, c + i, p.wt);
+        }
+      }
+    }
+  }
+  const int64_t yo = row * p.ys;
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const int c = (k * T + tx) * 8;
+    if (Q8) {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(v[k][i]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float s = block_scale(amax);
+      if (c < n) {
+        if ((tx & 15) == 0) p.scale[(int64_t)(c / kBlk) * p.scale_ld + row] = s;
+        uint8_t* q = static_cast<uint8_t*>(p.y) + yo + c;
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[k][4 * j] / s, v[k][4 * j + 1] / s), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[k][4 * j + 2] / s, v[k][4 * j + 3] / s), __NV_SATFINITE, __NV_E4M3);
+          w[j] = lo | (hi << 16);
+        }
+        if (c + 8 <= n) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+        else
+          for (int i = 0; i < 8 && c + i < n; ++i) q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+      }
+    } else {
+      if (c + 8 <= n) store8(p.y, yo + c, p.yt, v[k]);
+      else
+        for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.y, yo + c + i, p.yt, v[k][i]);
+    }
+  }
+}
+
+// the same for rows at any alignment: a warp per block of 128 columns and step
+template <int STEPS, bool Q8>
+__global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[32];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
+  grid_wait();
+  if (row >= p.rows) return;
+  const int n = p.n;
+  const int64_t xo = row * p.xs, ro = row * p.rs;
+  float v[STEPS][4];
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = (k * W + warp) * kBlk + i * 32 + lane;
+      v[k][i] = c < n ? load_act(p.x, xo + c, p.xt) : 0.f;
+    }
+  if (p.r) {
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (k * W + warp) * kBlk + i * 32 + lane;
+        if (c < n) v[k][i] += load_act(p.r, ro + c, p.rt);
+      }
+  }
+  if (p.h) {
+    const int64_t ho = row * p.hs;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (k * W + warp) * kBlk + i * 32 + lane;
+        if (c < n) store_act(p.h, ho + c, p.rt, v[k][i]);
+      }
+  }
+  if (p.norm) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fmaf(v[k][i], v[k][i], s);
+    const float inv = inv_rms(row_sum(s, red), n, p.eps);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (k * W + warp) * kBlk + i * 32 + lane;
+        v[k][i] *= inv;
+        if (p.w && c < n) v[k][i] *= load_act(p.w, c, p.wt);
+      }
+  }
+  const int64_t yo = row * p.ys;
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const int c0 = (k * W + warp) * kBlk;
+    if (c0 >= n) break;  // uniform in the warp
+    float s = 1.f;
+    if (Q8) {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax = max_nan(amax, fabsf(v[k][i]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      s = block_scale(amax);
+      if (lane == 0) p.scale[(int64_t)(c0 / kBlk) * p.scale_ld + row] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * 32 + lane;
+      if (c >= n) continue;
+      if (Q8) static_cast<uint8_t*>(p.y)[yo + c] = __nv_cvt_float_to_fp8(v[k][i] / s, __NV_SATFINITE, __NV_E4M3);
+      else store_act(p.y, yo + c, p.yt, v[k][i]);
+    }
+  }
+}
+
+// e4m3 of a weight matrix with a scale per 128 x 128 block: one CTA of 256 threads per block,
+// thread t takes columns 8 (t % 16) .. + 7 of rows t / 16, t / 16 + 16, ...
+__global__ void __launch_bounds__(256) weights_q8_kernel(const void* w, int wt, int64_t ws, int64_t n_out, int64_t n_in,
+                                                         uint8_t* q, int64_t qs, float* scale, int64_t kblocks) {
+  __shared__ float red[8];
+  grid_wait();
+  const int64_t r0 = (int64_t)blockIdx.y * kBlk, c0 = (int64_t)blockIdx.x * kBlk;
+  const int tr = threadIdx.x >> 4, tc = (threadIdx.x & 15) * 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float v[8][8], amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t r = r0 + tr + 16 * k;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = c0 + tc + i;
+      v[k][i] = r < n_out && c < n_in ? load_act(w, r * ws + c, wt) : 0.f;
+      amax = max_nan(amax, fabsf(v[k][i]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) red[warp] = amax;
+  __syncthreads();
+  amax = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) amax = max_nan(amax, red[i]);
+  const float s = block_scale(amax);
+  if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * kblocks + blockIdx.x] = s;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t r = r0 + tr + 16 * k;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = c0 + tc + i;
+      if (r < n_out && c < n_in) q[r * qs + c] = __nv_cvt_float_to_fp8(v[k][i] / s, __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+}
+
+template <bool Q8>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
+  auto on16 = [&](const void* ptr, int64_t stride, int bytes) {
+    return !ptr || p.rows == 1 || (stride * bytes) % 16 == 0;
+  };
+  const bool vec = on16(p.x, p.xs, dtype_bytes(p.xt)) && on16(p.r, p.rs, dtype_bytes(p.rt)) &&
+                   on16(p.h, p.hs, dtype_bytes(p.rt)) && on16(p.y, p.ys, Q8 ? 1 : dtype_bytes(p.yt));
+  const int per = vec ? 256 : kBlk;             // columns a warp covers per step
+  const int warps = (p.n + per - 1) / per;      // with one step per thread
+  int steps = 1;
+  while ((warps + steps - 1) / steps > 32) steps *= 2;
+  const int tpr = 32 * ((warps + steps - 1) / steps);
+  const int rpb = tpr == 32 ? 4 : 1;
+  const dim3 grid((unsigned)((p.rows + rpb - 1) / rpb)), block(tpr, rpb);
+  if (vec) {
+    if (steps == 1) return launch_dependent(norm_vec_kernel<1, Q8>, grid, block, 0, st, p);
+    if (steps == 2) return launch_dependent(norm_vec_kernel<2, Q8>, grid, block, 0, st, p);
+    return launch_dependent(norm_vec_kernel<4, Q8>, grid, block, 0, st, p);
+  }
+  if (steps == 1) return launch_dependent(norm_any_kernel<1, Q8>, grid, block, 0, st, p);
+  if (steps == 2) return launch_dependent(norm_any_kernel<2, Q8>, grid, block, 0, st, p);
+  if (steps == 4) return launch_dependent(norm_any_kernel<4, Q8>, grid, block, 0, st, p);
+  return launch_dependent(norm_any_kernel<8, Q8>, grid, block, 0, st, p);
+}
+
+// the arguments shared by the three entry points over rows
+harp_status check_rows(const char* who, int64_t rows, int64_t n, const void* x, int xt, int64_t xs, const void* r, int rt,
+                       int64_t rs, const void* w, int wt, const void* h, int64_t hs) {
+  if (rows < 0 || rows > 0x7fffffff) return set_error(HARP_ERR_INVALID_ARG, "%s: rows=%lld out of range", who, (long long)rows);
+  if (n < 1) return set_error(HARP_ERR_INVALID_ARG, "%s: n=%lld out of range", who, (long long)n);
+  if (n > kMaxCols) return set_error(HARP_ERR_UNSUPPORTED, "%s: n=%lld (at most %d columns)", who, (long long)n, kMaxCols);
+  if (!known_dtype(xt) || !known_dtype(rt) || !known_dtype(wt)) return set_error(HARP_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  if (!x) return set_error(HARP_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (xs < n || (r && rs < n) || (h && hs < n)) return set_error(HARP_ERR_INVALID_ARG, "%s: a row stride is below n", who);
+  if (!aligned_to(x, 16) || !aligned_to(r, 16) || !aligned_to(w, 16) || !aligned_to(h, 16))
+    return set_error(HARP_ERR_INVALID_ARG, "%s: device pointers must be 16-byte aligned", who);
+  return HARP_OK;
+}
+
+harp_status check_q8(const char* who, int64_t rows, int64_t n, const void* q, int64_t qs, const float* scale, int64_t ld) {
+  if (!q || !scale) return set_error(HARP_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned_to(q, 16) || !aligned_to(scale, 16)) return set_error(HARP_ERR_INVALID_ARG, "%s: device pointers must be 16-byte aligned", who);
+  if (qs < n || ld < rows) return set_error(HARP_ERR_INVALID_ARG, "%s: q_stride below n, or scale_ld below rows", who);
+  return HARP_OK;
+}
+
+harp_status launched(cudaError_t e, const char* who) {
+  return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_f32(int64_t rows, int n, float eps, const float* x, const float* residual, float* residual_out,
+                               float* y, cudaStream_t st) {
+  NormParams p{};
+  p.rows = rows;
+  p.n = n;
+  p.norm = 1;
+  p.eps = eps;
+  p.x = x;
+  p.r = residual;
+  p.h = residual_out;
+  p.y = y;
+  p.xs = p.rs = p.hs = p.ys = n;
+  p.xt = p.rt = p.wt = p.yt = DT_F32;
+  return launch_norm<false>(p, st);
+}
+
+}  // namespace harp
+
+using namespace harp;
+
+extern "C" {
+
+harp_status harp_rmsnorm(int64_t rows, int64_t n, float eps, const void* x, harp_dtype xt, int64_t x_stride,
+                         const void* residual, harp_dtype rt, int64_t r_stride, const void* weight, harp_dtype wt,
+                         void* residual_out, int64_t ro_stride, void* y, harp_dtype yt, int64_t y_stride, void* stream) {
+  harp_status s = check_rows("rmsnorm", rows, n, x, xt, x_stride, residual, rt, r_stride, weight, wt, residual_out, ro_stride);
+  if (s != HARP_OK) return s;
+  if (!y || !aligned_to(y, 16) || !known_dtype(yt) || y_stride < n)
+    return set_error(HARP_ERR_INVALID_ARG, "rmsnorm: y must be a 16-byte aligned f32, bf16 or f16 array with rows of n");
+  if (!(eps >= 0.f)) return set_error(HARP_ERR_INVALID_ARG, "rmsnorm: eps must not be negative");
+  if (rows == 0) return HARP_OK;
+  NormParams p{};
+  p.rows = rows; p.n = (int)n; p.norm = 1; p.eps = eps;
+  p.x = x; p.xt = xt; p.xs = x_stride;
+  p.r = residual; p.rt = rt; p.rs = r_stride;
+  p.w = weight; p.wt = wt;
+  p.h = residual_out; p.hs = ro_stride;
+  p.y = y; p.yt = yt; p.ys = y_stride;
+  return launched(launch_norm<false>(p, static_cast<cudaStream_t>(stream)), "rmsnorm launch");
+}
+
+harp_status harp_rmsnorm_q8(int64_t rows, int64_t n, float eps, const void* x, harp_dtype xt, int64_t x_stride,
+                            const void* residual, harp_dtype rt, int64_t r_stride, const void* weight, harp_dtype wt,
+                            void* residual_out, int64_t ro_stride, void* q, int64_t q_stride, float* scale,
+                            int64_t scale_ld, void* stream) {
+  harp_status s = check_rows("rmsnorm_q8", rows, n, x, xt, x_stride, residual, rt, r_stride, weight, wt, residual_out, ro_stride);
+  if (s == HARP_OK) s = check_q8("rmsnorm_q8", rows, n, q, q_stride, scale, scale_ld);
+  if (s != HARP_OK) return s;
+  if (!(eps >= 0.f)) return set_error(HARP_ERR_INVALID_ARG, "rmsnorm_q8: eps must not be negative");
+  if (rows == 0) return HARP_OK;
+  NormParams p{};
+  p.rows = rows; p.n = (int)n; p.norm = 1; p.eps = eps;
+  p.x = x; p.xt = xt; p.xs = x_stride;
+  p.r = residual; p.rt = rt; p.rs = r_stride;
+  p.w = weight; p.wt = wt;
+  p.h = residual_out; p.hs = ro_stride;
+  p.y = q; p.ys = q_stride; p.scale = scale; p.scale_ld = scale_ld;
+  return launched(launch_norm<true>(p, static_cast<cudaStream_t>(stream)), "rmsnorm_q8 launch");
+}
+
+harp_status harp_quantize_q8(int64_t rows, int64_t n, const void* x, harp_dtype xt, int64_t x_stride, void* q,
+                             int64_t q_stride, float* scale, int64_t scale_ld, void* stream) {
+  harp_status s = check_rows("quantize_q8", rows, n, x, xt, x_stride, nullptr, HARP_F32, 0, nullptr, HARP_F32, nullptr, 0);
+  if (s == HARP_OK) s = check_q8("quantize_q8", rows, n, q, q_stride, scale, scale_ld);
+  if (s != HARP_OK || rows == 0) return s;
+  NormParams p{};
+  p.rows = rows; p.n = (int)n;
+  p.x = x; p.xt = xt; p.xs = x_stride;
+  p.y = q; p.ys = q_stride; p.scale = scale; p.scale_ld = scale_ld;
+  return launched(launch_norm<true>(p, static_cast<cudaStream_t>(stream)), "quantize_q8 launch");
+}
+
+harp_status harp_quantize_weights_q8(int64_t n_out, int64_t n_in, const void* W, harp_dtype wt, int64_t w_stride, void* q,
+                                     int64_t q_stride, float* scale, void* stream) {
+  if (n_out < 1 || n_in < 1 || n_out > (1 << 22) || n_in > (1 << 22))
+    return set_error(HARP_ERR_INVALID_ARG, "quantize_weights_q8: n_out=%lld n_in=%lld out of range", (long long)n_out, (long long)n_in);
+  if (!known_dtype(wt)) return set_error(HARP_ERR_INVALID_ARG, "quantize_weights_q8: unknown dtype");
+  if (!W || !q || !scale) return set_error(HARP_ERR_INVALID_ARG, "quantize_weights_q8: null pointer");
+  if (!aligned_to(W, 16) || !aligned_to(q, 16) || !aligned_to(scale, 16))
+    return set_error(HARP_ERR_INVALID_ARG, "quantize_weights_q8: device pointers must be 16-byte aligned");
+  if (w_stride < n_in || q_stride < n_in) return set_error(HARP_ERR_INVALID_ARG, "quantize_weights_q8: a row stride is below n_in");
+  const int64_t kb = (n_in + kBlk - 1) / kBlk, nb = (n_out + kBlk - 1) / kBlk;
+  return launched(launch_dependent(weights_q8_kernel, dim3((unsigned)kb, (unsigned)nb), dim3(256), 0,
+                                   static_cast<cudaStream_t>(stream), W, (int)wt, w_stride, n_out, n_in,
+                                   static_cast<uint8_t*>(q), q_stride, scale, kb),
+                  "quantize_weights_q8 launch");
+}
+
+}  // extern "C"

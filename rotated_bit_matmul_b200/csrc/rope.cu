@@ -1,0 +1,313 @@
+// Rotary positions, and the write of keys and values into a paged cache.
+//
+//   pair i of the first rot_dim coordinates turns by the angle pos * f_i:
+//   (a, b) -> amplitude * (a cos - b sin, a sin + b cos);  the other coordinates are copied.
+//   Pairs are (i, i + rot_dim / 2) in the half layout, (2 i, 2 i + 1) in the interleaved one.
+//
+// The angle is taken as turns, pos * f_i / 2 pi, in fp64, reduced to [-1/2, 1/2] there and
+// only then handed to sincospi in fp32: positions of any int32 size keep full precision.
+// A CTA serves one token (or a share of its heads), so every pair's cosine and sine is
+// computed once per CTA and read from shared memory by all heads of q and k. The work is
+// bound by memory: each value is read and written once with 16-byte accesses; a unit of 16
+// coordinates (both halves of 8 pairs) belongs to one thread, so q may be rotated in place.
+#include "serve.cuh"
+#include "serve.h"
+
+#include <cmath>
+#include <new>
+
+namespace harp {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Params {
+  RopeTable t;
+  RopeCall c;
+};
+
+// where a token's keys and values go: element offset of its row in the pages of head 0, or -1
+__device__ __forceinline__ int64_t cache_row(const RopeCall& c, int64_t token, int pos) {
+  const int seq = c.seq_ids ? c.seq_ids[token] : (int)token;
+  const int64_t slot = pos / c.page_size;
+  if (seq < 0 || seq >= c.n_seqs || slot >= c.table_stride) {
+    report(c.status, 6 /* HARP_ERR_DEVICE_CHECK */, 90);
+    return -1;
+  }
+  const int page = c.table[(int64_t)seq * c.table_stride + slot];
+  if (page < 0 || page >= c.n_pages) {
+    report(c.status, 6, 91);
+    return -1;
+  }
+  return (int64_t)page * c.page_stride + (int64_t)(pos % c.page_size) * c.row_stride;
+}
+
+// VEC: 16-byte accesses on units of 16 coordinates; else single pairs at any alignment
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Params p) {
+  __shared__ float cs[kMaxRotPairs], sn[kMaxRotPairs];
+  __shared__ int64_t row_s;
+  const RopeCall& c = p.c;
+  const int64_t token = blockIdx.x;
+  const int hd = p.t.head_dim, rot = p.t.rot_dim, half = rot / 2;
+  grid_wait();
+  const int pos = c.positions[token];
+  if (pos < 0) return;  // uniform in the CTA
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double turns = (double)pos * p.t.turns[i];
+    float s, co;
+    sincospif((float)(2.0 * (turns - rint(turns))), &s, &co);
+    cs[i] = co * p.t.amplitude;
+    sn[i] = (c.inverse ? -s : s) * p.t.amplitude;
+  }
+  if (threadIdx.x == 0) row_s = c.kc ? cache_row(c, token, pos) : 0;
+  __syncthreads();
+  const int64_t row = row_s;
+  constexpr int U = VEC ? 16 : 2;   // coordinates of a unit
+  const int per_head = hd / U, rot_units = rot / U;
+  const int heads = c.q.heads + c.k.heads + c.v.heads;
+  const int units = heads * per_head;
+  for (int u = blockIdx.y * kThreads + threadIdx.x; u < units; u += gridDim.y * kThreads) {
+    int h = u / per_head;
+    const int j = u - h * per_head;
+    const bool is_q = h < c.q.heads, is_v = !is_q && h >= c.q.heads + c.k.heads;
+    const HeadRows& r = is_q ? c.q : is_v ? c.v : c.k;
+    if (!is_q) h -= is_v ? c.q.heads + c.k.heads : c.q.heads;
+    const bool turn = j < rot_units && !is_v;
+    // first coordinates of the unit's two runs of U / 2
+    const int e0 = !p.t.interleaved && turn ? j * (U / 2) : j * U;
+    const int e1 = !p.t.interleaved && turn ? e0 + half : e0 + U / 2;
+    const int64_t in = token * r.in_ts + h * r.in_hs;
+    void* out;
+    int64_t o;
+    int ot;
+    if (is_q || !c.kc) {
+      out = r.out;
+      o = token * r.out_ts + h * r.out_hs;
+      ot = c.yt;
+    } else {
+      if (row < 0) continue;
+      out = is_v ? c.vc : c.kc;
+      o = row + h * c.head_stride;
+      ot = c.ct;
+    }
+    const int pair = j * (U / 2);
+    if (VEC) {
+      float a[8], b[8];
+      const Raw8 ra = raw_load8(r.in, in + e0, c.xt), rb = raw_load8(r.in, in + e1, c.xt);
+      raw_unpack8(ra, c.xt, a);
+      raw_unpack8(rb, c.xt, b);
+      if (turn) {
+        float co[8], si[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          *reinterpret_cast<float4*>(co + i) = *reinterpret_cast<const float4*>(cs + pair + i);
+          *reinterpret_cast<float4*>(si + i) = *reinterpret_cast<const float4*>(sn + pair + i);
+        }
+        if (p.t.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
+            a[2 * i] = x0 * co[i] - y0 * si[i];
+            a[2 * i + 1] = x0 * si[i] + y0 * co[i];
+            b[2 * i] = x1 * co[i + 4] - y1 * si[i + 4];
+            b[2 * i + 1] = x1 * si[i + 4] + y1 * co[i + 4];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = a[i], y = b[i];
+            a[i] = x * co[i] - y * si[i];
+            b[i] = x * si[i] + y * co[i];
+          }
+        }
+      }
+      store8(out, o + e0, ot, a);
+      store8(out, o + e1, ot, b);
+    } else {
+      float a = load_act(r.in, in + e0, c.xt), b = load_act(r.in, in + e1, c.xt);
+      if (turn) {
+        const float x = a, y = b;
+        a = x * cs[pair] - y * sn[pair];
+        b = x * sn[pair] + y * cs[pair];
+      }
+      store_act(out, o + e0, ot, a);
+      store_act(out, o + e1, ot, b);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeTable& t, const RopeCall& c, cudaStream_t st) {
+  Params p{t, c};
+  // 16-byte accesses: whole units of 16 coordinates, and every row of every tensor on a
+  // 16-byte boundary
+  bool vec = t.head_dim % 16 == 0 && t.rot_dim % 16 == 0;
+  auto rows16 = [&](const void* ptr, int64_t ts, int64_t hs, int dt) {
+    const int b = dtype_bytes(dt);
+    if (ptr) vec = vec && aligned_to(ptr, 16) && (ts * b) % 16 == 0 && (hs * b) % 16 == 0;
+  };
+  for (const HeadRows* r : {&c.q, &c.k, &c.v})
+    if (r->heads) {
+      rows16(r->in, r->in_ts, r->in_hs, c.xt);
+      rows16(r->out, r->out_ts, r->out_hs, c.yt);
+    }
+  if (c.kc) rows16(c.kc, c.page_stride, c.head_stride, c.ct), rows16(c.vc, c.row_stride, c.head_stride, c.ct);
+  // a CTA serves a whole token, unless there are too few tokens to fill the GPU
+  const int64_t units = (int64_t)(c.q.heads + c.k.heads + c.v.heads) * (t.head_dim / (vec ? 16 : 2));
+  const int64_t most = (units + kThreads - 1) / kThreads;
+  int64_t share = (2 * 148 + c.tokens - 1) / c.tokens;
+  if (share > most) share = most;
+  const dim3 grid((unsigned)c.tokens, (unsigned)share);
+  if (vec) return launch_dependent(rope_kernel<true>, grid, dim3(kThreads), 0, st, p);
+  return launch_dependent(rope_kernel<false>, grid, dim3(kThreads), 0, st, p);
+}
+
+harp_status check_cache(const char* who, const harp_kv_cache* c) {
+  if (!c || !c->k || !c->v) return set_error(HARP_ERR_INVALID_ARG, "%s: null cache", who);
+  if (c->dtype != HARP_BF16 && c->dtype != HARP_F16) return set_error(HARP_ERR_UNSUPPORTED, "%s: the cache holds bf16 or f16", who);
+  if (c->n_pages < 1 || c->n_pages > 0x7fffffff || c->n_kv_heads < 1 || c->n_kv_heads > 65535 || c->head_dim < 2 ||
+      c->head_dim > 2 * kMaxRotPairs || c->head_dim % 2)
+    return set_error(HARP_ERR_INVALID_ARG, "%s: bad cache sizes", who);
+  if (c->page_size < 1 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
+    return set_error(HARP_ERR_INVALID_ARG, "%s: page_size=%d must be a power of two, at most 4096", who, c->page_size);
+  if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || c->page_stride % 8 || c->head_stride % 8 || c->row_stride % 8 ||
+      c->row_stride < c->head_dim || c->head_stride < 0 || c->page_stride < 0)
+    return set_error(HARP_ERR_INVALID_ARG, "%s: cache rows must lie on 16-byte boundaries, row_stride at least head_dim", who);
+  return HARP_OK;
+}
+
+}  // namespace harp
+
+using namespace harp;
+
+extern "C" {
+
+harp_status harp_rope_frequencies(int rot_dim, double base, harp_rope_scaling scaling, double factor, double original,
+                                  double low, double high, double* freq) {
+  if (!freq) return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: null pointer");
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > 2 * kMaxRotPairs)
+    return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: rot_dim=%d must be even, 2..%d", rot_dim, 2 * kMaxRotPairs);
+  if (!(base > 1.0) || !std::isfinite(base)) return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: base must be above 1");
+  if (scaling != HARP_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor)))
+    return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: factor must be at least 1");
+  const bool parts = scaling == HARP_ROPE_BANDS || scaling == HARP_ROPE_RAMP;
+  if (parts && !(original > 0.0 && low > 0.0 && high > low && std::isfinite(original) && std::isfinite(high)))
+    return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: needs original > 0 and 0 < low < high");
+  if (scaling < HARP_ROPE_NONE || scaling > HARP_ROPE_RAMP) return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: unknown scaling");
+  if (scaling == HARP_ROPE_NTK && rot_dim < 4) return set_error(HARP_ERR_INVALID_ARG, "rope_frequencies: NTK needs rot_dim >= 4");
+  const double two_pi = 6.283185307179586476925;
+  const double b = scaling == HARP_ROPE_NTK ? base * pow(factor, (double)rot_dim / (rot_dim - 2)) : base;
+  double first = 0, last = 1;
+  if (scaling == HARP_ROPE_RAMP) {
+    // the pair indices that turn `high` and `low` times in `original` positions
+    auto index = [&](double turns) { return rot_dim * log(original / (turns * two_pi)) / (2 * log(base)); };
+    first = fmax(floor(index(high)), 0.0);
+    last = fmin(ceil(index(low)), rot_dim - 1.0);
+    if (last <= first) last = first + 0.001;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = pow(b, -2.0 * i / rot_dim);
+    double keep = 1.0;
+    if (scaling == HARP_ROPE_LINEAR) keep = 0.0;
+    if (scaling == HARP_ROPE_BANDS) keep = fmin(1.0, fmax(0.0, (original * f / two_pi - low) / (high - low)));
+    if (scaling == HARP_ROPE_RAMP) keep = 1.0 - fmin(1.0, fmax(0.0, (i - first) / (last - first)));
+    freq[i] = scaling == HARP_ROPE_NONE || scaling == HARP_ROPE_NTK ? f : f * keep + f / factor * (1.0 - keep);
+  }
+  return HARP_OK;
+}
+
+harp_status harp_rope_create(harp_rope* out, int head_dim, int rot_dim, int interleaved, const double* freq, double amplitude) {
+  if (!out || !freq) return set_error(HARP_ERR_INVALID_ARG, "rope_create: null pointer");
+  *out = nullptr;
+  if (head_dim < 2 || head_dim > 2 * kMaxRotPairs || head_dim % 2 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2)
+    return set_error(HARP_ERR_INVALID_ARG, "rope_create: head_dim=%d and rot_dim=%d must be even, rot_dim <= head_dim <= %d",
+                     head_dim, rot_dim, 2 * kMaxRotPairs);
+  if (!std::isfinite(amplitude)) return set_error(HARP_ERR_INVALID_ARG, "rope_create: amplitude must be finite");
+  for (int i = 0; i < rot_dim / 2; ++i)
+    if (!std::isfinite(freq[i]) || std::fabs(freq[i]) > 1e3)
+      return set_error(HARP_ERR_INVALID_ARG, "rope_create: frequency %d is not a finite number of at most 1000", i);
+  harp_rope_s* r = new (std::nothrow) harp_rope_s();
+  if (!r) return set_error(HARP_ERR_INVALID_ARG, "rope_create: out of host memory");
+  r->t.head_dim = head_dim;
+  r->t.rot_dim = rot_dim;
+  r->t.interleaved = interleaved != 0;
+  r->t.amplitude = (float)amplitude;
+  for (int i = 0; i < rot_dim / 2; ++i) r->t.turns[i] = freq[i] / 6.283185307179586476925;
+  *out = r;
+  return HARP_OK;
+}
+
+harp_status harp_rope_destroy(harp_rope rope) {
+  delete rope;
+  return HARP_OK;
+}
+
+harp_status harp_rope_apply(harp_rope rope, int64_t tokens, int heads, const int32_t* positions, const void* x, harp_dtype xt,
+                            int64_t x_token_stride, int64_t x_head_stride, void* y, harp_dtype yt, int64_t y_token_stride,
+                            int64_t y_head_stride, int inverse, void* stream) {
+  if (!rope || !positions || !x || !y) return set_error(HARP_ERR_INVALID_ARG, "rope_apply: null pointer");
+  if (tokens < 0 || tokens > 0x7fffffff || heads < 1 || heads > 65535) return set_error(HARP_ERR_INVALID_ARG, "rope_apply: bad sizes");
+  if (!known_dtype(xt) || !known_dtype(yt)) return set_error(HARP_ERR_INVALID_ARG, "rope_apply: unknown dtype");
+  if (!aligned_to(positions, 4) || !aligned_to(x, dtype_bytes(xt)) || !aligned_to(y, dtype_bytes(yt)))
+    return set_error(HARP_ERR_INVALID_ARG, "rope_apply: a pointer is not aligned to its type");
+  if (x == y && (xt != yt || x_token_stride != y_token_stride || x_head_stride != y_head_stride))
+    return set_error(HARP_ERR_INVALID_ARG, "rope_apply: in place needs equal dtypes and strides");
+  if (tokens == 0) return HARP_OK;
+  RopeCall c{};
+  c.tokens = tokens;
+  c.positions = positions;
+  c.q = HeadRows{x, x_token_stride, x_head_stride, y, y_token_stride, y_head_stride, heads};
+  c.xt = xt;
+  c.yt = yt;
+  c.inverse = inverse != 0;
+  const cudaError_t e = launch_rope(rope->t, c, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
+}
+
+harp_status harp_rope_append(harp_rope rope, const harp_kv_cache* cache, int64_t tokens, int n_heads, const int32_t* positions,
+                             const int32_t* seq_ids, int n_seqs, const int32_t* page_table, int64_t max_pages, const void* q,
+                             int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, harp_dtype xt,
+                             void* q_out, harp_dtype yt, int64_t o_token_stride, int64_t o_head_stride, void* stream) {
+  harp_status s = check_cache("rope_append", cache);
+  if (s != HARP_OK) return s;
+  if (!rope || !positions || !page_table || !q || !k || !v || !q_out) return set_error(HARP_ERR_INVALID_ARG, "rope_append: null pointer");
+  if (tokens < 0 || tokens > 0x7fffffff || n_heads < 1 || n_heads > 65535 || n_seqs < 1 || max_pages < 1)
+    return set_error(HARP_ERR_INVALID_ARG, "rope_append: bad sizes");
+  if (cache->head_dim != rope->t.head_dim) return set_error(HARP_ERR_INVALID_ARG, "rope_append: the cache's head_dim is not the plan's");
+  if (!seq_ids && tokens > n_seqs) return set_error(HARP_ERR_INVALID_ARG, "rope_append: more tokens than sequences need seq_ids");
+  if (!known_dtype(xt) || !known_dtype(yt)) return set_error(HARP_ERR_INVALID_ARG, "rope_append: unknown dtype");
+  if (!aligned_to(positions, 4) || !aligned_to(seq_ids, 4) || !aligned_to(page_table, 4) || !aligned_to(q, dtype_bytes(xt)) ||
+      !aligned_to(k, dtype_bytes(xt)) || !aligned_to(v, dtype_bytes(xt)) || !aligned_to(q_out, dtype_bytes(yt)))
+    return set_error(HARP_ERR_INVALID_ARG, "rope_append: a pointer is not aligned to its type");
+  if (q == q_out && (xt != yt || q_token_stride != o_token_stride || q_head_stride != o_head_stride))
+    return set_error(HARP_ERR_INVALID_ARG, "rope_append: in place needs equal dtypes and strides");
+  if (tokens == 0) return HARP_OK;
+  RopeCall c{};
+  if ((s = device_status_for_kernels(&c.status)) != HARP_OK) return s;
+  c.tokens = tokens;
+  c.positions = positions;
+  c.q = HeadRows{q, q_token_stride, q_head_stride, q_out, o_token_stride, o_head_stride, n_heads};
+  c.k = HeadRows{k, k_token_stride, k_head_stride, nullptr, 0, 0, cache->n_kv_heads};
+  c.v = HeadRows{v, v_token_stride, v_head_stride, nullptr, 0, 0, cache->n_kv_heads};
+  c.xt = xt;
+  c.yt = yt;
+  c.kc = cache->k;
+  c.vc = cache->v;
+  c.ct = cache->dtype;
+  c.page_size = cache->page_size;
+  c.n_pages = cache->n_pages;
+  c.page_stride = cache->page_stride;
+  c.head_stride = cache->head_stride;
+  c.row_stride = cache->row_stride;
+  c.table = page_table;
+  c.table_stride = max_pages;
+  c.n_seqs = n_seqs;
+  c.seq_ids = seq_ids;
+  const cudaError_t e = launch_rope(rope->t, c, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "rope_append launch: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

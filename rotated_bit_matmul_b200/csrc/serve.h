@@ -1,0 +1,82 @@
+// Host-side launch interface of the serving operators, for the entry points and the stack.
+#pragma once
+
+#include "harp_internal.h"
+
+namespace harp {
+
+constexpr int kMaxRotPairs = 128;  // head_dim up to 256
+
+// Rotary table: turns per position of every pair (frequency / 2 pi), kept by value in the
+// launch parameters, so a plan owns no device memory.
+struct RopeTable {
+  double turns[kMaxRotPairs];
+  float amplitude;
+  int head_dim, rot_dim, interleaved;
+};
+
+// Rows of heads: element (token, head, d) at base + token * ts + head * hs + d.
+struct HeadRows {
+  const void* in;
+  int64_t in_ts, in_hs;
+  void* out;  // null: rows go to the cache
+  int64_t out_ts, out_hs;
+  int heads;
+};
+
+struct RopeCall {
+  int64_t tokens;
+  const int32_t* positions;  // negative: the row is skipped
+  HeadRows q, k, v;          // heads 0: absent
+  int xt, yt;                // inputs; q.out (and k.out) type
+  int inverse;
+  // cache write (kc set)
+  void* kc;
+  void* vc;
+  int ct, page_size;
+  int64_t n_pages, page_stride, head_stride, row_stride;
+  const int32_t* table;      // [n_seqs][table_stride]
+  int64_t table_stride;
+  int n_seqs;
+  const int32_t* seq_ids;    // null: token t belongs to sequence t
+  int* status;
+};
+cudaError_t launch_rope(const RopeTable& t, const RopeCall& c, cudaStream_t st);
+
+struct AttnCall {
+  int n_seqs, n_heads, n_kv, head_dim, dt;
+  const void* q;
+  int64_t q_ss, q_hs;        // strides of q between sequences and heads
+  const void* kc;
+  const void* vc;
+  int page_size;
+  int64_t n_pages, page_stride, head_stride, row_stride, max_pages;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  int len_add;               // keys of sequence s: lens[s] + len_add
+  int keep_negative;         // rows of negative length are left as they were (else zeros)
+  float scale;
+  int window;                // 0: every earlier key
+  void* out;
+  int64_t o_ss, o_hs;
+  float* lse;                // [n_seqs][n_heads] or null
+  void* ws;
+  int* status;
+};
+size_t attention_ws_bytes(int head_dim);
+cudaError_t launch_attention(const AttnCall& c, cudaStream_t st);
+// null when the shape is one the kernels are built for, else what is not supported
+const char* attention_refuses(int n_seqs, int n_heads, int n_kv, int head_dim, int dt);
+
+cudaError_t launch_rmsnorm_f32(int64_t rows, int n, float eps, const float* x, const float* residual, float* residual_out,
+                               float* y, cudaStream_t st);
+
+// argument checks of a cache and its page table
+harp_status check_cache(const char* who, const harp_kv_cache* c);
+
+}  // namespace harp
+
+struct harp_rope_s {
+  harp::RopeTable t;
+};

@@ -2,6 +2,7 @@
 // layers: RMSNorm, residual adds, SiLU * up, and the key/value-group broadcast of a
 // one-key attention (its output is the value), around harp linear forwards.
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -11,6 +12,7 @@
 
 #include "common.cuh"
 #include "decode.h"
+#include "serve.h"
 
 using namespace harp;
 
@@ -387,6 +389,29 @@ void setup_fused(harp_stack_s* S) {
   S->fused = true;
 }
 
+// buffers of a step over a cache behind those of stack_ws: q and the attention's output in
+// the cache's type, and the attention's partials
+struct CachedWs {
+  void *q, *a, *attn;
+  size_t bytes;
+};
+
+CachedWs cached_ws(const harp_stack_s* S, int batch, void* base) {
+  const size_t row = 2 * (size_t)batch * S->n_heads * S->head_dim;
+  CachedWs w{};
+  size_t off = a256(stack_ws(S, batch, nullptr).bytes);
+  auto take = [&](size_t bytes) -> void* {
+    void* r = base ? static_cast<char*>(base) + off : nullptr;
+    off = a256(off + bytes);
+    return r;
+  };
+  w.q = take(row);
+  w.a = take(row);
+  w.attn = take(attention_ws_bytes(S->head_dim));
+  w.bytes = off;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -518,6 +543,122 @@ harp_status harp_stack_step(harp_stack S, int batch, const void* x, harp_dtype x
   store_kernel<<<eltwise_blocks(B * H), 256, 0, st>>>(w.x, out, ot, B * H);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return sfail(HARP_ERR_CUDA, std::string("stack_step launch: ") + cudaGetErrorString(e));
+  return HARP_OK;
+}
+
+harp_status harp_stack_cached_workspace_size(harp_stack stack, int batch, size_t* bytes) {
+  if (!stack || !bytes) return sfail(HARP_ERR_INVALID_ARG, "stack_cached_workspace_size: null pointer");
+  if (batch < 1 || batch > 256) return sfail(HARP_ERR_INVALID_ARG, "stack_cached_workspace_size: batch out of range");
+  *bytes = cached_ws(stack, batch, nullptr).bytes;
+  return HARP_OK;
+}
+
+harp_status harp_stack_step_cached(harp_stack S, int batch, const void* x, harp_dtype xt, void* out, harp_dtype ot,
+                                   harp_rope rope, const harp_kv_cache* cache, int64_t layer_stride, const int32_t* positions,
+                                   const int32_t* page_table, int64_t max_pages, int window, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  if (!S || !x || !out || !rope || !positions || !page_table) return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: null pointer");
+  if (batch < 1 || batch > 256) return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: batch out of range");
+  if (xt < 0 || xt > 2 || ot < 0 || ot > 2) return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: unknown dtype");
+  harp_status s = check_cache("stack_step_cached", cache);
+  if (s != HARP_OK) return s;
+  if (cache->n_kv_heads != S->n_kv_heads || cache->head_dim != S->head_dim || rope->t.head_dim != S->head_dim)
+    return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: the cache's or the rotary plan's heads are not the stack's");
+  if (const char* why = attention_refuses(batch, S->n_heads, S->n_kv_heads, S->head_dim, cache->dtype))
+    return sfail(HARP_ERR_UNSUPPORTED, std::string("stack_step_cached: ") + why);
+  if (layer_stride < 0 || layer_stride % 8 || (S->n_layers > 1 && layer_stride == 0))
+    return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: layer_stride must be a positive multiple of 8");
+  if (max_pages < 1 || max_pages * cache->page_size > 0x7fffff00 || window < 0)
+    return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: max_pages or window out of range");
+  if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(page_table)) & 3u)
+    return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: positions and page_table must be 4-byte aligned");
+  const size_t need = cached_ws(S, batch, nullptr).bytes;
+  if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return sfail(HARP_ERR_WORKSPACE, "stack_step_cached: workspace of " + std::to_string(need) +
+                                         " bytes (256-byte aligned) needed");
+  int* status = nullptr;
+  if ((s = device_status_for_kernels(&status)) != HARP_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  StackWs w = stack_ws(S, batch, workspace);
+  CachedWs cw = cached_ws(S, batch, workspace);
+  const int64_t B = batch, H = S->hidden, F = S->ffn;
+  const int64_t hd = S->head_dim, dq = S->n_heads * hd, dkv = S->n_kv_heads * hd;
+  const int ct = cache->dtype;
+  auto launched = [&](cudaError_t e) {
+    if (s == HARP_OK && e != cudaSuccess)
+      s = sfail(HARP_ERR_CUDA, std::string("stack_step_cached launch: ") + cudaGetErrorString(e));
+  };
+  RopeCall rc{};
+  rc.tokens = B;
+  rc.positions = positions;
+  rc.q = HeadRows{w.q, dq, hd, cw.q, dq, hd, S->n_heads};
+  rc.k = HeadRows{w.k, dkv, hd, nullptr, 0, 0, S->n_kv_heads};
+  rc.v = HeadRows{w.v, dkv, hd, nullptr, 0, 0, S->n_kv_heads};
+  rc.xt = DT_F32;
+  rc.yt = rc.ct = ct;
+  rc.page_size = cache->page_size;
+  rc.n_pages = cache->n_pages;
+  rc.page_stride = cache->page_stride;
+  rc.head_stride = cache->head_stride;
+  rc.row_stride = cache->row_stride;
+  rc.table = page_table;
+  rc.table_stride = max_pages;
+  rc.n_seqs = batch;
+  rc.status = status;
+  AttnCall ac{};
+  ac.n_seqs = batch;
+  ac.n_heads = S->n_heads;
+  ac.n_kv = S->n_kv_heads;
+  ac.head_dim = S->head_dim;
+  ac.dt = ct;
+  ac.q = cw.q;
+  ac.q_ss = ac.o_ss = dq;
+  ac.q_hs = ac.o_hs = hd;
+  ac.page_size = cache->page_size;
+  ac.n_pages = cache->n_pages;
+  ac.page_stride = cache->page_stride;
+  ac.head_stride = cache->head_stride;
+  ac.row_stride = cache->row_stride;
+  ac.max_pages = max_pages;
+  ac.table = page_table;
+  ac.table_stride = max_pages;
+  ac.lens = positions;
+  ac.len_add = 1;  // the new token attends to itself
+  ac.scale = 1.0f / sqrtf((float)hd);
+  ac.window = window;
+  ac.out = cw.a;
+  ac.ws = cw.attn;
+  ac.status = status;
+  convert_kernel<<<eltwise_blocks(B * H), 256, 0, st>>>(x, xt, w.x, B * H);
+  launched(launch_rmsnorm_f32(B, (int)H, S->eps, w.x, nullptr, nullptr, w.n1, st));
+  for (int l = 0; l < S->n_layers && s == HARP_OK; ++l) {
+    const Layer* L[7];
+    for (int i = 0; i < 7; ++i) L[i] = &S->layers[7 * l + i]->L;
+    s = linear_forward(*L[0], batch, w.n1, DT_F32, H, w.q, DT_F32, dq, w.lin, st);
+    if (s == HARP_OK) s = linear_forward(*L[1], batch, w.n1, DT_F32, H, w.k, DT_F32, dkv, w.lin, st);
+    if (s == HARP_OK) s = linear_forward(*L[2], batch, w.n1, DT_F32, H, w.v, DT_F32, dkv, w.lin, st);
+    if (s != HARP_OK) break;
+    rc.kc = static_cast<uint16_t*>(cache->k) + l * layer_stride;
+    rc.vc = static_cast<uint16_t*>(cache->v) + l * layer_stride;
+    ac.kc = rc.kc;
+    ac.vc = rc.vc;
+    launched(launch_rope(rope->t, rc, st));
+    launched(launch_attention(ac, st));
+    if (s == HARP_OK) s = linear_forward(*L[3], batch, cw.a, ct, dq, w.o, DT_F32, H, w.lin, st);
+    launched(launch_rmsnorm_f32(B, (int)H, S->eps, w.o, w.x, w.x, w.n1, st));
+    if (s == HARP_OK) s = linear_forward(*L[4], batch, w.n1, DT_F32, H, w.g, DT_F32, F, w.lin, st);
+    if (s == HARP_OK) s = linear_forward(*L[5], batch, w.n1, DT_F32, H, w.u, DT_F32, F, w.lin, st);
+    if (s != HARP_OK) break;
+    silu_mul_kernel<<<eltwise_blocks(B * F), 256, 0, st>>>(w.g, w.u, B * F);
+    s = linear_forward(*L[6], batch, w.g, DT_F32, F, w.o, DT_F32, H, w.lin, st);
+    // the residual's addition runs with the next block's norm, or alone after the last block
+    if (l + 1 < S->n_layers) launched(launch_rmsnorm_f32(B, (int)H, S->eps, w.o, w.x, w.x, w.n1, st));
+    else add_kernel<<<eltwise_blocks(B * H), 256, 0, st>>>(w.x, w.o, B * H);
+  }
+  if (s != HARP_OK) return s;
+  store_kernel<<<eltwise_blocks(B * H), 256, 0, st>>>(w.x, out, ot, B * H);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return sfail(HARP_ERR_CUDA, std::string("stack_step_cached launch: ") + cudaGetErrorString(e));
   return HARP_OK;
 }
 

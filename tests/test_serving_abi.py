@@ -1,0 +1,200 @@
+"""CPU checks of the serving operators' entry points: validation runs before any CUDA call, so
+none of these touch a GPU."""
+import ctypes
+import math
+
+import pytest
+
+FAKE = 1 << 20  # aligned, never dereferenced: validation fails first
+OFF4, OFF2, OFF1 = FAKE + 4, FAKE + 2, FAKE + 1
+F32, BF16, F16 = 0, 1, 2
+INVALID, UNSUPPORTED, CUDA, WORKSPACE = 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from rotated_bit_matmul_b200 import build_lib, _lib
+    build_lib.build()
+    return _lib.load()
+
+
+def _changed(base, /, **kw):
+    args = dict(base)
+    for k, v in kw.items():
+        assert k in args, k
+        args[k] = v
+    return list(args.values())
+
+
+NORM = dict(rows=4, n=256, eps=1e-5, x=FAKE, xt=BF16, xs=256, r=FAKE, rt=BF16, rs=256, w=FAKE, wt=BF16, h=FAKE, hs=256, y=FAKE,
+            yt=BF16, ys=256, st=None)
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(rows=-1), INVALID), (dict(rows=1 << 31), INVALID), (dict(n=0), INVALID), (dict(n=32769, xs=40000, rs=40000, hs=40000), UNSUPPORTED),
+    (dict(eps=-1.0), INVALID), (dict(eps=math.nan), INVALID), (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(x=OFF4), INVALID),
+    (dict(y=OFF4), INVALID), (dict(w=OFF4), INVALID), (dict(xt=3), INVALID), (dict(rt=7), INVALID), (dict(yt=-1), INVALID),
+    (dict(xs=255), INVALID), (dict(rs=100), INVALID), (dict(hs=0), INVALID), (dict(ys=255), INVALID), (dict(rows=0), 0)])
+def test_rmsnorm_refusals(lib, kw, err):
+    assert lib.harp_rmsnorm(*_changed(NORM, **kw)) == err
+    if err:
+        assert lib.harp_last_error()
+
+
+Q8 = dict(rows=4, n=256, eps=1e-5, x=FAKE, xt=BF16, xs=256, r=None, rt=F32, rs=0, w=None, wt=F32, h=None, hs=0, q=FAKE, qs=256,
+          s=FAKE, ld=4, st=None)
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(q=None), INVALID), (dict(s=None), INVALID), (dict(q=OFF4), INVALID), (dict(s=OFF4), INVALID), (dict(qs=255), INVALID),
+    (dict(ld=3), INVALID), (dict(eps=-1e-9), INVALID), (dict(rows=0, ld=0), 0)])
+def test_q8_refusals(lib, kw, err):
+    assert lib.harp_rmsnorm_q8(*_changed(Q8, **kw)) == err
+    if "eps" not in kw:
+        d = {k: v for k, v in {**Q8, **kw}.items() if k not in ("eps", "r", "rt", "rs", "w", "wt", "h", "hs")}
+        assert lib.harp_quantize_q8(*d.values()) == err
+
+
+W8 = dict(n_out=256, n_in=256, W=FAKE, wt=BF16, ws=256, q=FAKE, qs=256, s=FAKE, st=None)
+
+
+@pytest.mark.parametrize("kw", [dict(n_out=0), dict(n_in=0), dict(n_in=(1 << 22) + 1), dict(W=None), dict(q=None), dict(s=OFF4),
+                                dict(W=OFF4), dict(wt=5), dict(ws=255), dict(qs=255)])
+def test_weights_q8_refusals(lib, kw):
+    assert lib.harp_quantize_weights_q8(*_changed(W8, **kw)) == INVALID
+
+
+L8 = dict(n_in=256, n_out=256, codes=FAKE, stride=256, scale=FAKE, st=None)
+
+
+@pytest.mark.parametrize("kw", [dict(n_in=0), dict(n_out=0), dict(n_out=(1 << 22) + 1), dict(codes=None), dict(scale=None),
+                                dict(codes=FAKE + 8), dict(stride=255), dict(stride=264), dict(n_in=300)])
+def test_layer8_refusals(lib, kw):
+    h = ctypes.c_void_p()
+    assert lib.harp_create_layer8(ctypes.byref(h), *_changed(L8, **kw)) == INVALID and not h.value
+    assert lib.harp_create_layer8(None, *L8.values()) == INVALID
+    assert lib.harp_linear8_fwd(None, 1, FAKE, 256, FAKE, 4, FAKE, BF16, 256, None) == INVALID
+    assert lib.harp_destroy_layer8(None) == 0
+
+
+FREQ = dict(rot=64, base=1e4, scaling=3, factor=8.0, original=4096.0, low=1.0, high=4.0)
+
+
+@pytest.mark.parametrize("kw", [dict(rot=0), dict(rot=63), dict(rot=258), dict(base=1.0), dict(base=math.inf), dict(base=math.nan),
+                                dict(scaling=5), dict(scaling=-1), dict(factor=0.5), dict(factor=math.nan), dict(original=0.0),
+                                dict(low=0.0), dict(low=4.0), dict(high=math.inf), dict(scaling=2, rot=2)])
+def test_rope_frequencies_refusals(lib, kw):
+    f = (ctypes.c_double * 128)()
+    assert lib.harp_rope_frequencies(*_changed(FREQ, **kw), f) == INVALID
+    assert lib.harp_rope_frequencies(*FREQ.values(), None) == INVALID
+    assert lib.harp_rope_frequencies(*FREQ.values(), f) == 0
+
+
+def _plan(lib, hd=64, rot=64, f=None, amplitude=1.0):
+    h = ctypes.c_void_p()
+    freq = (ctypes.c_double * 128)(*([0.5] * 128)) if f is None else f
+    return lib.harp_rope_create(ctypes.byref(h), hd, rot, 0, freq, amplitude), h
+
+
+def test_rope_create_refusals(lib):
+    bad = (ctypes.c_double * 128)(math.nan)
+    for st, h in (_plan(lib, 63), _plan(lib, 64, 66), _plan(lib, 258, 64), _plan(lib, 64, 0), _plan(lib, 64, 3), _plan(lib, f=bad),
+                  _plan(lib, f=(ctypes.c_double * 128)(2e3)), _plan(lib, amplitude=math.inf)):
+        assert st == INVALID and not h.value
+    assert lib.harp_rope_create(None, 64, 64, 0, bad, 1.0) == INVALID
+    assert lib.harp_rope_destroy(None) == 0
+    st, h = _plan(lib)  # a plan needs no device
+    assert st == 0 and lib.harp_rope_destroy(h) == 0
+
+
+@pytest.fixture(scope="module")
+def rope(lib):
+    st, h = _plan(lib)
+    assert st == 0
+    yield h
+    lib.harp_rope_destroy(h)
+
+
+def test_rope_apply_refusals(lib, rope):
+    A = dict(rope=rope, tokens=4, heads=2, pos=FAKE, x=FAKE, xt=BF16, xts=128, xhs=64, y=FAKE + 4096, yt=BF16, yts=128, yhs=64, inv=0, st=None)
+    for kw in (dict(rope=None), dict(pos=None), dict(x=None), dict(y=None), dict(tokens=-1), dict(heads=0), dict(heads=70000), dict(xt=3),
+               dict(yt=9), dict(pos=OFF2), dict(x=OFF1), dict(y=OFF1), dict(y=FAKE, yt=F32), dict(y=FAKE, yts=64)):
+        assert lib.harp_rope_apply(*_changed(A, **kw)) == INVALID, kw
+    assert lib.harp_rope_apply(*_changed(A, tokens=0)) == 0
+
+
+def _cache(**kw):
+    from rotated_bit_matmul_b200._lib import KVCache
+    f = dict(k=FAKE, v=FAKE, dtype=BF16, n_kv_heads=2, head_dim=64, page_size=16, n_pages=8, page_stride=2048, head_stride=1024, row_stride=64)
+    f.update(kw)
+    return KVCache(*f.values())
+
+
+BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(dtype=F32), UNSUPPORTED), (dict(n_pages=0), INVALID),
+              (dict(n_kv_heads=0), INVALID), (dict(head_dim=63), INVALID), (dict(head_dim=512), INVALID), (dict(page_size=0), INVALID),
+              (dict(page_size=12), INVALID), (dict(page_size=8192), INVALID), (dict(k=FAKE + 8), INVALID), (dict(page_stride=4), INVALID),
+              (dict(head_stride=12), INVALID), (dict(row_stride=56), INVALID)]
+
+
+@pytest.mark.parametrize("kw,err", BAD_CACHES)
+def test_cache_refusals(lib, rope, kw, err):
+    c = _cache(**kw)
+    assert lib.harp_rope_append(rope, ctypes.byref(c), 4, 2, FAKE, None, 4, FAKE, 8, FAKE, 128, 64, FAKE, 128, 64, FAKE, 128, 64, BF16,
+                                FAKE + 4096, BF16, 128, 64, None) == err
+    assert lib.harp_paged_attention(ctypes.byref(c), 4, 2, FAKE, 128, 64, FAKE, 8, FAKE, 1.0, 0, FAKE, 128, 64, None, FAKE, 1 << 30, None) == err
+
+
+def test_rope_append_refusals(lib, rope):
+    c = _cache()
+    A = dict(rope=rope, cache=ctypes.byref(c), tokens=4, heads=4, pos=FAKE, ids=None, seqs=4, table=FAKE, pages=8, q=FAKE, qts=256, qhs=64,
+             k=FAKE, kts=128, khs=64, v=FAKE, vts=128, vhs=64, xt=BF16, out=FAKE + 4096, yt=BF16, ots=256, ohs=64, st=None)
+    for kw in (dict(rope=None), dict(cache=None), dict(pos=None), dict(table=None), dict(q=None), dict(k=None), dict(v=None), dict(out=None),
+               dict(tokens=-1), dict(heads=0), dict(seqs=0), dict(pages=0), dict(tokens=5), dict(xt=4), dict(yt=4), dict(pos=OFF2),
+               dict(ids=OFF2), dict(table=OFF1), dict(q=OFF1), dict(out=OFF1), dict(out=FAKE, yt=F32)):
+        assert lib.harp_rope_append(*_changed(A, **kw)) == INVALID, kw
+    assert lib.harp_rope_append(*_changed(A, tokens=0)) == 0
+    wide = _cache(head_dim=128, row_stride=128)
+    assert lib.harp_rope_append(*_changed(A, cache=ctypes.byref(wide))) == INVALID
+
+
+def test_paged_attention_refusals(lib):
+    c = _cache()
+    n = ctypes.c_size_t()
+    assert lib.harp_paged_attention_workspace_size(64, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.harp_paged_attention_workspace_size(64, None) == INVALID
+    assert lib.harp_paged_attention_workspace_size(0, ctypes.byref(n)) == INVALID
+    A = dict(cache=ctypes.byref(c), seqs=4, heads=4, q=FAKE, qs=256, qh=64, table=FAKE, pages=8, lens=FAKE, scale=1.0, window=0, out=FAKE,
+             os=256, oh=64, lse=None, ws=FAKE, bytes=n.value, st=None)
+    for kw, err in ((dict(cache=None), INVALID), (dict(q=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
+                    (dict(out=None), INVALID), (dict(seqs=-1), INVALID), (dict(seqs=70000), INVALID), (dict(heads=3), INVALID),
+                    (dict(heads=0), INVALID), (dict(pages=0), INVALID), (dict(pages=1 << 30), INVALID), (dict(window=-1), INVALID),
+                    (dict(scale=math.nan), INVALID), (dict(q=OFF2), INVALID), (dict(qs=255), INVALID), (dict(oh=63), INVALID),
+                    (dict(lens=OFF2), INVALID), (dict(lse=OFF2), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 16), WORKSPACE),
+                    (dict(bytes=n.value - 1), WORKSPACE)):
+        assert lib.harp_paged_attention(*_changed(A, **kw)) == err, kw
+    assert lib.harp_paged_attention(*_changed(A, seqs=0)) == 0
+    for hd, err in ((40, UNSUPPORTED), (80, UNSUPPORTED), (224, UNSUPPORTED)):
+        d = _cache(head_dim=hd, row_stride=hd)
+        assert lib.harp_paged_attention(*_changed(A, cache=ctypes.byref(d), bytes=1 << 40)) == err
+
+
+def test_stack_step_cached_refuses_null(lib, rope):
+    c = _cache()
+    n = ctypes.c_size_t()
+    assert lib.harp_stack_cached_workspace_size(None, 1, ctypes.byref(n)) == INVALID
+    assert lib.harp_stack_step_cached(None, 1, FAKE, 0, FAKE, 0, rope, ctypes.byref(c), 0, FAKE, FAKE, 8, 0, FAKE, 1 << 30, None) == INVALID
+
+
+def test_binding_refuses_cpu_tensors_and_bad_shapes():
+    torch = pytest.importorskip("torch")
+    import rotated_bit_matmul_b200 as rb
+    x = torch.zeros(4, 128)
+    for call in (lambda: rb.harp_rmsnorm(x), lambda: rb.harp_rmsnorm_q8(x), lambda: rb.harp_quantize_q8(x),
+                 lambda: rb.harp_quantize_weights_q8(x), lambda: rb.HarpLinear8(x, x), lambda: rb.HarpCache(x, x),
+                 lambda: rb.HarpRope(64)(x.view(4, 2, 64), torch.zeros(4, dtype=torch.int32)),
+                 lambda: rb.HarpRope(64, scaling="other"), lambda: rb.HarpRope(64, frequencies=[1.0])):
+        with pytest.raises(ValueError):
+            call()
+    assert rb.HarpRope(8, base=100.0).frequencies[1] == pytest.approx(100.0 ** -0.25, rel=1e-14)
+    with pytest.raises(AttributeError):
+        rb.no_such_operator
