@@ -440,8 +440,8 @@ harp_status harp_rope_apply(harp_rope rope, int64_t tokens, int heads, const int
  * p * page_stride + h * head_stride + r * row_stride of k and of v. Position j of sequence s
  * lies in page page_table[s * max_pages + j / page_size], row j % page_size.
  * dtype bf16 or f16; page_size a power of two, at most 4096; head_dim even, at most 256; strides
- * multiples of 8; k and v 16-byte aligned. Page indices outside [0, n_pages) are never
- * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93). */
+ * positive multiples of 8; k and v 16-byte aligned. Page indices outside [0, n_pages) are never
+ * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93) and takes their rows as 0. */
 typedef struct {
   void* k;
   void* v;
@@ -468,7 +468,8 @@ harp_status harp_rope_append(harp_rope rope, const harp_kv_cache* cache, int64_t
  *   len = seq_lens[s] (the new token's own row included); window 0: all of them.
  * Query head h reads key head h / (n_heads / n_kv_heads). A sequence of length 0 gets zeros
  * and lse -infinity; rows of negative length are left as they were; a length beyond
- * max_pages * page_size is cut to it and reported. Rows outside the mask are not read.
+ * max_pages * page_size is cut to it and reported. What cache rows outside the mask hold (NaN
+ * included) has no effect.
  *   q, out : device [n_seqs][n_heads][head_dim] of the cache's dtype, rows on 4-byte boundaries.
  *   lse    : device fp32 [n_seqs][n_heads], log sum exp of the scaled scores, or NULL.
  *   n_seqs <= 65535; head_dim 32, 64, 96, 128, 192 or 256 (else HARP_ERR_UNSUPPORTED).

@@ -153,6 +153,21 @@ bool encode_map_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, ui
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_map_4d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                   const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i < 3) s[i] = stride_bytes[i];
+  }
+  return fn(tm, dt, 4, const_cast<void*>(base), d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int xq_words_per_row(int64_t n_in, int bits) { return (int)(bits == 3 ? n_in : n_in / 2); }
 
 LinearWs linear_ws_layout(const Layer& L, int batch, void* base) {

@@ -8,19 +8,22 @@
 // of its rate; the 128-row tcgen05 tile would be filled to an eighth or less by one token's
 // heads). Softmax statistics and outputs are fp32 with a running maximum.
 //
-// Split. The tiles of 64 keys of all (sequence, key head) pairs form one line, which is cut
-// into equal shares, one per CTA, from the lengths on the device: any mix of lengths is
-// balanced without the host knowing it, and a captured launch stays valid as lengths grow.
-// A pair that lies in one share is finished there. One that is cut leaves an fp32 partial
+// Split. The key tiles of all (sequence, key head) pairs form one line, which is cut into equal
+// shares, one per worker, from the lengths on the device: any mix of lengths is balanced
+// without the host knowing it, and a captured launch stays valid as lengths grow. A pair
+// counts its tiles and kPairCost more on the line, the time its q, first page and output
+// take. A pair that lies in one share is finished there. One that is cut leaves an fp32 partial
 // (maximum, sum, unnormalised output) per share in the workspace, and join_kernel adds them
 // in the order of the keys, so results do not depend on timing.
 //
-// Inside a CTA each of four warps owns 16 keys of every tile and everything it needs for
-// them: it looks up the pages, copies K and V rows with cp.async into its own ring of
-// stages, and keeps its own maximum, sum and output. The loop has no CTA barrier; the warps
-// meet only where a pair ends. Rows outside the mask are not read: their bytes in shared
-// memory are zero-filled, so what a page holds behind a sequence's end (NaN included) has
-// no effect. The copies run ahead across pair borders, so the ring stays full.
+// A worker is a CTA's four warps, each with 16 keys of every tile of 64, or, with at least
+// one pair per warp of the GPU, a single warp with tiles of 16: then no warp ever waits for
+// another. Each warp has everything it needs for its keys: it looks up the pages, asks for
+// the K and V rows with TMA (one box per page and 64 columns, 128-byte swizzle) into its own
+// ring of stages, and keeps its own maximum, sum and output. The loop has no CTA barrier; the
+// warps of a CTA worker meet only where a pair ends. The copies run ahead across pair
+// borders, so the ring stays full. Rows outside the mask have weight 0 and their V rows are
+// zeroed, so what a page holds behind a sequence's end (NaN included) has no effect.
 //
 // The probabilities enter the second product as hi + lo halves of the cache's type (two
 // products into one accumulator): a single bf16 p would add an error of 2^-9 per key, as
@@ -28,27 +31,35 @@
 #include "serve.cuh"
 #include "serve.h"
 
+#include <algorithm>
+
 namespace harp {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 64;   // keys per tile; 16 per warp
+constexpr int kWarpKeys = 16;  // keys of a tile per warp
 constexpr int kRows = 16;   // query heads per tile
-constexpr int kMaxCtas = 2 * 148;
+constexpr int kMaxWorkers = 2 * 148 * kWarps;
+// what a pair costs beside its tiles, in tiles of 64 and of 16 keys
+constexpr int kPairCost = 2, kPairCostWarp = 3;
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = 4;  // heads per CTA of the join
 
 struct Params {
+  CUtensorMap tm_k, tm_v;  // (column, row, head, page) of 2-byte elements, box {64, box_rows, 1, 1}
   AttnCall c;
   int group;       // query heads per key head
   int hblocks;     // tiles of kRows query heads per key head
   int units;       // n_kv * hblocks: pairs per sequence
-  int ctas;        // CTAs of the attention kernel
+  int workers;
+  int tile_shift;  // log2 keys per tile
+  int pair_cost;
+  int box_rows;    // rows of a TMA box: the page size, at most 16
   int page_shift;
   float scale_log2;
-  float* part_o;   // [ctas][2][kRows][head_dim]
-  float* part_ml;  // [ctas][2][kRows][2]
+  float* part_o;   // [workers][2][kRows][head_dim]: [0] of the pair that began in an earlier
+  float* part_ml;  // [workers][2][kRows][2]          share, [1] of the one that goes on in a later
 };
 
 __device__ __forceinline__ int keys_of(const Params& p, int seq) {
@@ -60,22 +71,26 @@ __device__ __forceinline__ int first_key(const Params& p, int len) {
 }
 // tiles of a sequence of `len` keys per (key head, head block)
 __device__ __forceinline__ int tiles_of(const Params& p, int len) {
-  return len == 0 ? 0 : (len - 1) / kTile - first_key(p, len) / kTile + 1;
+  return len == 0 ? 0 : ((len - 1) >> p.tile_shift) - (first_key(p, len) >> p.tile_shift) + 1;
+}
+__device__ __forceinline__ int cost_of(const Params& p, int len) {
+  const int t = tiles_of(p, len);
+  return t ? t + p.pair_cost : 0;
 }
 
-// Position of a tile on the line of all tiles.
+// A place on the line: place 0 .. pair_cost - 1 of a pair stands before its first tile.
 struct Where {
-  int seq, unit, tile, ntiles;  // tile in [0, ntiles) of the pair
-  int64_t first;                // the pair's first tile on the line
+  int seq, unit, ntiles, len;
+  int64_t first;  // the pair's first place
 };
 
-// Sum of tiles over all sequences, and where tile `at` lies. All threads of the CTA.
-// `red` holds blockDim.x + 1 + blockDim.x / 32 int64.
+// Length of the line, with its prefix sums by thread in `red` (blockDim.x + 1 +
+// blockDim.x / 32 int64). All threads of the CTA.
 __device__ int64_t line_total(const Params& p, int64_t* red, int per) {
   int64_t s = 0;
   for (int i = 0; i < per; ++i) {
     const int seq = threadIdx.x * per + i;
-    if (seq < p.c.n_seqs) s += tiles_of(p, keys_of(p, seq));
+    if (seq < p.c.n_seqs) s += cost_of(p, keys_of(p, seq));
   }
   s *= p.units;
   // inclusive scan in the warp, then over the warps
@@ -105,36 +120,39 @@ __device__ Where locate(const Params& p, const int64_t* red, int per, int64_t at
   }
   Where w;
   int64_t base = red[lo];
+  int cost;
   w.seq = lo * per;
   for (;; ++w.seq) {
-    w.ntiles = tiles_of(p, keys_of(p, w.seq));
-    const int64_t n = (int64_t)w.ntiles * p.units;
+    w.len = keys_of(p, w.seq);
+    cost = cost_of(p, w.len);
+    const int64_t n = (int64_t)cost * p.units;
     if (at < base + n) break;
     base += n;
   }
-  const int64_t r = at - base;
-  w.unit = (int)(r / w.ntiles);
-  w.tile = (int)(r - (int64_t)w.unit * w.ntiles);
-  w.first = at - w.tile;
+  w.ntiles = cost - p.pair_cost;
+  w.unit = (int)((at - base) / cost);
+  w.first = base + (int64_t)w.unit * cost;
   return w;
 }
 
 // shares of the line: none is empty
-__device__ __forceinline__ int shares(const Params& p, int64_t total) { return (int)min((int64_t)p.ctas, total); }
-__device__ __forceinline__ int64_t share_begin(int64_t total, int ctas, int64_t c) { return c * total / ctas; }
-// the CTA whose share holds tile x
-__device__ __forceinline__ int share_of(int64_t total, int ctas, int64_t x) {
-  return (int)(((x + 1) * ctas - 1) / total);
-}
+__device__ __forceinline__ int shares(const Params& p, int64_t total) { return (int)min((int64_t)p.workers, total); }
+__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int64_t c) { return c * total / n; }
+// the share that holds place x
+__device__ __forceinline__ int share_of(int64_t total, int n, int64_t x) { return (int)(((x + 1) * n - 1) / total); }
 
 // ------------------------------------------------------------------ matrix helpers
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int x, int row, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -160,34 +178,41 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Row pitch 2 HD bytes; 16-byte chunk c of row r lies at chunk c ^ key(r), which puts the 8
-// rows that one ldmatrix reads on distinct banks (a pitch that is an odd multiple of 64
-// bytes shifts every other row by half the banks already).
-template <int HD>
+// K or V rows of a stage: blocks of 64 columns, each kWarpKeys rows of 128 bytes whose 16-byte
+// chunk c lies at chunk c ^ (row & 7) (the TMA's 128-byte swizzle: the 8 rows of one ldmatrix
+// fall on distinct banks).
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  const int key = (HD / 8) % 8 == 0 ? (r & 7) : ((r >> 1) & 3);
-  return (uint32_t)(r * HD * 2 + ((c ^ key) << 4));
+  return (uint32_t)((c >> 3) * (kWarpKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <int HD>
+template <int HD, int W>
 struct Cfg {
-  static constexpr int kStageWarp = 2 * 16 * HD * 2;             // K and V rows of one warp's stage
-  static constexpr int kStages = HD <= 32 ? 8 : HD <= 64 ? 6 : HD <= 96 ? 4 : HD <= 192 ? 3 : 2;
+  static constexpr int kBlocks = (HD + 63) / 64;
+  static constexpr int kOperand = kBlocks * kWarpKeys * 128;      // K or V of one warp's stage
+  static constexpr int kStageWarp = 2 * kOperand;
+  static constexpr int kStages = HD <= 64 ? 6 : HD <= 192 ? 3 : 2;
   static constexpr int kCtasPerSm = HD <= 128 ? 2 : 1;
   static constexpr int kRing = kWarps * kStages * kStageWarp;
-  static constexpr int kMerge = 2 * kRows * HD * 4 + 2 * kRows * 2 * 4;  // two warps' outputs and statistics
-  static constexpr int kQ = HD > 128 ? kRows * HD * 2 : 0;        // wide heads read q from shared memory
-  static constexpr int kSmem = kRing + kMerge + kQ;
+  // W > 1: two warps' outputs and statistics; also the prefix sums of the line
+  static constexpr int kScan = (kThreads + 1 + kThreads / 32) * 8;
+  static constexpr int kMerge = W > 1 ? 2 * kRows * HD * 4 + 2 * kRows * 2 * 4 : (kScan + 15) / 16 * 16;
+  static constexpr int kQ = HD > 128 ? kBlocks * kRows * 128 : 0;  // wide heads read q from shared memory
+  static constexpr int kSmem = kRing + kMerge + kQ + kWarps * kStages * 8;
+  static_assert(kMerge >= kScan, "the prefix sums lie in the merge boxes");
 };
 
-template <int HD, int DT>
-__global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<HD>;
-  constexpr int ST = C::kStages, KS = HD / 16, CH = HD / 8;
-  extern __shared__ __align__(128) uint8_t smem[];
+template <int HD, int DT, int W>
+__global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<HD, W>;
+  constexpr int ST = C::kStages, KS = HD / 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
   int64_t* red = reinterpret_cast<int64_t*>(smem + C::kRing);  // before the merge boxes are in use
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const AttnCall& c = p.c;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kMerge + C::kQ) + warp * ST;
+  if (lane < ST) mbar_init(&full[lane], 1);
+  fence_mbar_init();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   grid_wait();
 
   const int per = (c.n_seqs + kThreads - 1) / kThreads;
@@ -201,88 +226,121 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
     if (c.lse)
       for (int i = threadIdx.x; i < c.n_heads; i += kThreads) c.lse[(int64_t)s * c.n_heads + i] = -INFINITY;
   }
-  const int ctas = shares(p, total);
-  if ((int)blockIdx.x >= ctas) {
+  const int n = shares(p, total);
+  const int worker = W == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle needs it; the launch gives it
+    report(c.status, 6, 94);
+    return;
+  }
+  if (worker >= n) {
     grid_release();
     return;
   }
-  const int64_t begin = share_begin(total, ctas, blockIdx.x), end = share_begin(total, ctas, blockIdx.x + 1);
+  const int64_t begin = share_begin(total, n, worker), end = share_begin(total, n, worker + 1);
 
-  const uint32_t ring = smem_u32(smem) + warp * ST * C::kStageWarp;
+  uint8_t* ring = smem + warp * ST * C::kStageWarp;
+  const uint32_t ring_s = smem_u32(ring);
   float* merge_o = reinterpret_cast<float*>(smem + C::kRing);        // [2][kRows][HD]
   float* merge_ml = merge_o + 2 * kRows * HD;                        // [2][kRows][2]
-  const uint32_t q_s = smem_u32(smem + C::kRing + C::kMerge);
+  uint8_t* q_sm = smem + C::kRing + C::kMerge;
+
+  // A share's part of a pair: tiles [tile, stop). Places before the first tile count as 0, so a
+  // share that ends there has none of the pair.
+  struct Cursor {
+    Where w;
+    int start, tile, stop;
+  };
+  auto enter = [&](Cursor& u) {  // the part of u.w's pair in this share
+    const int64_t zero = u.w.first + p.pair_cost;
+    u.start = first_key(p, u.w.len);
+    u.tile = (int)max(begin - zero, (int64_t)0);
+    u.stop = (int)min(end - zero, (int64_t)u.w.ntiles);
+  };
+  auto next_pair = [&](Cursor& u) -> bool {  // false at the end of the share
+    u.w.first += u.w.ntiles + p.pair_cost;
+    if (u.w.first >= end) return false;
+    if (++u.w.unit == p.units) {
+      u.w.unit = 0;
+      do {
+        ++u.w.seq;
+        u.w.len = keys_of(p, u.w.seq);
+        u.w.ntiles = tiles_of(p, u.w.len);
+      } while (u.w.ntiles == 0);
+    }
+    enter(u);
+    return u.stop > u.tile;
+  };
+  Cursor use;
+  use.w = locate(p, red, per, begin);
+  enter(use);
+  bool have = use.stop > use.tile || next_pair(use);  // a share may end before its only pair's first tile
+  const int box_rows = p.box_rows, boxes = kWarpKeys / box_rows;
 
   // ---------------- load cursor: runs ST - 1 tiles ahead of the products
-  const Where w0 = locate(p, red, per, begin);
-  Where lw = w0;
-  int64_t l_at = begin;
-  int l_len = keys_of(p, lw.seq), l_start = first_key(p, l_len);
-  // lane j < 16 holds the page of the warp's key j of the tile the cursor stands on
-  auto page_ahead = [&]() -> int {
-    const int key = (l_start / kTile + lw.tile) * kTile + warp * 16 + (lane & 15);
-    return key >= l_start && key < l_len ? c.table[(int64_t)lw.seq * c.table_stride + (key >> p.page_shift)] : -1;
+  Cursor ld = use;
+  bool more = have;
+  auto first_of = [&](const Cursor& u, int tile) -> int {  // this warp's first key of the tile
+    return (((u.start >> p.tile_shift) + tile) << p.tile_shift) + (W == 1 ? 0 : warp * kWarpKeys);
   };
-  int page = page_ahead();
+  // lane j < boxes: page of its box's rows in the tile under the cursor (-1: outside the mask)
+  auto page_ahead = [&]() -> int {
+    const int key = first_of(ld, ld.tile) + lane * box_rows;
+    return lane < boxes && key < ld.w.len && key + box_rows > ld.start
+               ? c.table[(int64_t)ld.w.seq * c.table_stride + (key >> p.page_shift)] : -1;
+  };
+  int page = more ? page_ahead() : -1;
   auto load_tile = [&](int slot) {
-    const uint32_t dst = ring + slot * C::kStageWarp;
-    const int key = (l_start / kTile + lw.tile) * kTile + warp * 16 + (lane & 15);
-    int64_t off = -1;
-    if (key >= l_start && key < l_len) {
-      if (page >= 0 && page < c.n_pages)
-        off = page * c.page_stride + (int64_t)(key & (c.page_size - 1)) * c.row_stride +
-              (int64_t)(lw.unit / p.hblocks) * c.head_stride;
-      else report(c.status, 6 /* HARP_ERR_DEVICE_CHECK */, 92);  // a row that is not there reads as zeros
+    uint8_t* dst = ring + slot * C::kStageWarp;
+    const int key = first_of(ld, ld.tile) + lane * box_rows;
+    const bool in_mask = lane < boxes && key < ld.w.len && key + box_rows > ld.start;
+    const bool good = in_mask && page >= 0 && page < c.n_pages;
+    if (__any_sync(0xffffffffu, in_mask && !good)) {  // rows that are not there read as zeros
+      if (in_mask && !good) {
+        report(c.status, 6 /* HARP_ERR_DEVICE_CHECK */, 92);
+        for (int b = 0; b < 2 * C::kBlocks; ++b)
+          for (int i = 0; i < box_rows * 8; ++i)
+            *reinterpret_cast<uint4*>(dst + b * kWarpKeys * 128 + lane * box_rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
     }
+    const unsigned live = __ballot_sync(0xffffffffu, good);
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * box_rows * 128 * 2 * C::kBlocks);
+    __syncwarp();
+    if (good) {
+      const int row = key & (c.page_size - 1), head = ld.w.unit / p.hblocks;
+      const uint32_t at = smem_u32(dst) + lane * box_rows * 128;
 #pragma unroll
-    for (int i = 0; i < CH * 16 / 32; ++i) {
-      const int x = i * 32 + lane, r = x / CH, ch = x % CH;
-      const int64_t ro = __shfl_sync(0xffffffffu, off, r);
-      const int64_t eo = (ro < 0 ? 0 : ro) + ch * 8;
-      const uint32_t at = chunk_at<HD>(r, ch);
-      cp_async16(dst + at, static_cast<const uint16_t*>(c.kc) + eo, ro >= 0);
-      cp_async16(dst + 16 * HD * 2 + at, static_cast<const uint16_t*>(c.vc) + eo, ro >= 0);
+      for (int b = 0; b < C::kBlocks; ++b) {
+        tma_load_4d(at + b * kWarpKeys * 128, &p.tm_k, &full[slot], b * 64, row, head, page);
+        tma_load_4d(at + C::kOperand + b * kWarpKeys * 128, &p.tm_v, &full[slot], b * 64, row, head, page);
+      }
     }
     // advance, and ask for the next tile's pages
-    ++l_at;
-    if (l_at < end) {
-      if (++lw.tile == lw.ntiles) {
-        lw.tile = 0;
-        if (++lw.unit == p.units) {
-          lw.unit = 0;
-          do {
-            ++lw.seq;
-            l_len = keys_of(p, lw.seq);
-            lw.ntiles = tiles_of(p, l_len);
-          } while (lw.ntiles == 0);
-          l_start = first_key(p, l_len);
-        }
-      }
-      page = page_ahead();
-    }
+    if (++ld.tile >= ld.stop) more = next_pair(ld);
+    page = more ? page_ahead() : -1;
   };
 
   int put = 0;
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i) {
-    if (l_at < end) load_tile(put++);
-    cp_commit();
-  }
+  for (int i = 0; i < ST - 1; ++i)
+    if (more) load_tile(put++);
 
   // ---------------- products
-  Where w = w0;
-  int len = keys_of(p, w.seq), start = first_key(p, len);
-  int64_t at = begin;
   int slot = 0;
-  while (at < end) {
-    const int kvh = w.unit / p.hblocks, hb = w.unit - kvh * p.hblocks;
+  uint32_t phase = 0;
+  int in_flight = put, lost_slot = 0;  // stages asked for and not yet waited for
+  uint32_t lost_phase = 0;
+  bool ok = true;
+  while (have) {
+    const int kvh = use.w.unit / p.hblocks, hb = use.w.unit - kvh * p.hblocks;
     const int h0 = kvh * p.group + hb * kRows, nh = min(kRows, p.group - hb * kRows);
-    const int tile_end = (int)min((int64_t)w.ntiles, w.tile + (end - at));
+    const int len = use.w.len, start = use.start;
     const int row = lane >> 2;
     // q rows `row` and `row + 8` as A fragments (rows beyond the group are zero)
     uint32_t qf[HD > 128 ? 1 : KS][4];
     {
-      const uint16_t* q = static_cast<const uint16_t*>(c.q) + w.seq * c.q_ss + h0 * c.q_hs;
+      const uint16_t* q = static_cast<const uint16_t*>(c.q) + use.w.seq * c.q_ss + h0 * c.q_hs;
       auto pair_at = [&](int r, int d) -> uint32_t {
         if (r >= nh) return 0u;
         return *reinterpret_cast<const uint32_t*>(q + r * c.q_hs + d);
@@ -291,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
         __syncthreads();  // the last pair's q is no longer read
         for (int i = threadIdx.x; i < kRows * HD / 2; i += kThreads) {
           const int r = i / (HD / 2), d = (i % (HD / 2)) * 2;
-          *reinterpret_cast<uint32_t*>(smem + C::kRing + C::kMerge + chunk_at<HD>(r, d >> 3) + (d & 7) * 2) = pair_at(r, d);
+          *reinterpret_cast<uint32_t*>(q_sm + chunk_at(r, d >> 3) + (d & 7) * 2) = pair_at(r, d);
         }
         __syncthreads();
       } else {
@@ -312,25 +370,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    for (int tile = w.tile; tile < tile_end; ++tile) {
-      cp_wait<ST - 2>();
+    for (int tile = use.tile; tile < use.stop; ++tile) {
+      if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, c.status, 95));
+        if (ok) {
+          --in_flight;
+        } else {  // reported: ask for nothing more and run to the end
+          more = false;
+          lost_slot = slot;
+          lost_phase = phase;
+        }
+      }
       __syncwarp();
       // the stage refilled here was read before this __syncwarp
-      if (l_at < end) {
+      if (more) {
         load_tile(put);
         put = put + 1 == ST ? 0 : put + 1;
+        ++in_flight;
       }
-      cp_commit();
-      const uint32_t ks = ring + slot * C::kStageWarp, vs = ks + 16 * HD * 2;
+      const uint32_t ks = ring_s + slot * C::kStageWarp, vs = ks + C::kOperand;
+      const int first = first_of(use, tile);
+      const bool inside = first >= start && first + kWarpKeys <= len;
+      if (!inside) {  // weight 0 does not silence a NaN: V rows outside the mask become zeros
+        uint8_t* v = ring + slot * C::kStageWarp + C::kOperand;
+        const int r = lane >> 1, key = first + r;
+        if (key < start || key >= len)
+#pragma unroll
+          for (int i = 0; i < C::kBlocks * 4; ++i)
+            *reinterpret_cast<uint4*>(v + (i >> 2) * (kWarpKeys * 128) + r * 128 + (lane & 1) * 64 + (i & 3) * 16) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
       // scores of 16 keys: two blocks of 8
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t b[4];
-        ldsm4(b, ks + chunk_at<HD>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+        ldsm4(b, ks + chunk_at((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
         if (HD > 128) {
           uint32_t a[4];
-          ldsm4(a, q_s + chunk_at<HD>(lane & 15, 2 * k + (lane >> 4)));
+          ldsm4(a, smem_u32(q_sm) + chunk_at(lane & 15, 2 * k + (lane >> 4)));
           mma16816<DT>(s[0], a, b[0], b[1]);
           mma16816<DT>(s[1], a, b[2], b[3]);
         } else {
@@ -338,14 +417,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
           mma16816<DT>(s[1], qf[HD > 128 ? 0 : k], b[2], b[3]);
         }
       }
-      const int key0 = (start / kTile + tile) * kTile + warp * 16 + (lane & 3) * 2;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + j * 8 + (e & 1);
-          s[j][e] = key >= start && key < len ? s[j][e] * p.scale_log2 : -INFINITY;
-        }
+        for (int e = 0; e < 4; ++e) s[j][e] *= p.scale_log2;
+      if (!inside) {
+        const int key0 = first + (lane & 3) * 2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + j * 8 + (e & 1);
+            if (key < start || key >= len) s[j][e] = -INFINITY;
+          }
+      }
       float n0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
       float n1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
 #pragma unroll
@@ -357,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
       n1 = fmaxf(m1, n1);
       if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
         // -inf: no live key yet, nothing to rescale
-        const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
+        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
@@ -374,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float a = exp2f(s[j][0] - z0), b = exp2f(s[j][1] - z0), d = exp2f(s[j][2] - z1), e = exp2f(s[j][3] - z1);
+        const float a = ex2(s[j][0] - z0), b = ex2(s[j][1] - z0), d = ex2(s[j][2] - z1), e = ex2(s[j][3] - z1);
         l0 += a + b;
         l1 += d + e;
         hi[2 * j] = pack2(a, b, DT);
@@ -386,91 +471,95 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
 #pragma unroll
       for (int i = 0; i < HD / 16; ++i) {
         uint32_t b[4];
-        ldsm4t(b, vs + chunk_at<HD>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * i + (lane >> 4)));
+        ldsm4t(b, vs + chunk_at((lane & 7) + (((lane >> 3) & 1) << 3), 2 * i + (lane >> 4)));
         mma16816<DT>(o[2 * i], hi, b[0], b[1]);
         mma16816<DT>(o[2 * i + 1], hi, b[2], b[3]);
         mma16816<DT>(o[2 * i], lo, b[0], b[1]);
         mma16816<DT>(o[2 * i + 1], lo, b[2], b[3]);
       }
-      slot = slot + 1 == ST ? 0 : slot + 1;
+      if (++slot == ST) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-
-    // ---------------- join the four warps (1 -> 0 and 3 -> 2, then 2 -> 0), in key order
 #pragma unroll
     for (int x = 1; x < 4; x <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, x);
       l1 += __shfl_xor_sync(0xffffffffu, l1, x);
     }
+
+    // ---------------- join the four warps (1 -> 0 and 3 -> 2, then 2 -> 0), in key order
+    if (W > 1) {
 #pragma unroll
-    for (int step = 1; step <= 2; ++step) {
-      const bool gives = step == 1 ? (warp & 1) : warp == 2, takes = step == 1 ? !(warp & 1) : warp == 0;
-      const int box = step == 1 ? warp >> 1 : 0;
-      float* bo = merge_o + box * kRows * HD;
-      float* bml = merge_ml + box * kRows * 2;
-      __syncthreads();  // the boxes are free
-      if (gives) {
+      for (int step = 1; step <= 2; ++step) {
+        const bool gives = step == 1 ? (warp & 1) : warp == 2, takes = step == 1 ? !(warp & 1) : warp == 0;
+        const int box = step == 1 ? warp >> 1 : 0;
+        float* bo = merge_o + box * kRows * HD;
+        float* bml = merge_ml + box * kRows * 2;
+        __syncthreads();  // the boxes are free
+        if (gives) {
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          const int d = i * 8 + (lane & 3) * 2;
-          *reinterpret_cast<float2*>(bo + row * HD + d) = make_float2(o[i][0], o[i][1]);
-          *reinterpret_cast<float2*>(bo + (row + 8) * HD + d) = make_float2(o[i][2], o[i][3]);
+          for (int i = 0; i < HD / 8; ++i) {
+            const int d = i * 8 + (lane & 3) * 2;
+            *reinterpret_cast<float2*>(bo + row * HD + d) = make_float2(o[i][0], o[i][1]);
+            *reinterpret_cast<float2*>(bo + (row + 8) * HD + d) = make_float2(o[i][2], o[i][3]);
+          }
+          if ((lane & 3) == 0) {
+            bml[row * 2] = m0;
+            bml[row * 2 + 1] = l0;
+            bml[(row + 8) * 2] = m1;
+            bml[(row + 8) * 2 + 1] = l1;
+          }
         }
-        if ((lane & 3) == 0) {
-          bml[row * 2] = m0;
-          bml[row * 2 + 1] = l0;
-          bml[(row + 8) * 2] = m1;
-          bml[(row + 8) * 2 + 1] = l1;
-        }
-      }
-      __syncthreads();
-      if (takes) {
-        const float a0 = bml[row * 2], a1 = bml[(row + 8) * 2];
-        const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-        const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
-        const float g0 = a0 == -INFINITY ? 0.f : exp2f(a0 - n0), g1 = a1 == -INFINITY ? 0.f : exp2f(a1 - n1);
-        l0 = l0 * f0 + bml[row * 2 + 1] * g0;
-        l1 = l1 * f1 + bml[(row + 8) * 2 + 1] * g1;
-        m0 = n0;
-        m1 = n1;
+        __syncthreads();
+        if (takes) {
+          const float a0 = bml[row * 2], a1 = bml[(row + 8) * 2];
+          const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+          const float g0 = a0 == -INFINITY ? 0.f : ex2(a0 - n0), g1 = a1 == -INFINITY ? 0.f : ex2(a1 - n1);
+          l0 = l0 * f0 + bml[row * 2 + 1] * g0;
+          l1 = l1 * f1 + bml[(row + 8) * 2 + 1] * g1;
+          m0 = n0;
+          m1 = n1;
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          const int d = i * 8 + (lane & 3) * 2;
-          const float2 x = *reinterpret_cast<const float2*>(bo + row * HD + d);
-          const float2 y = *reinterpret_cast<const float2*>(bo + (row + 8) * HD + d);
-          o[i][0] = o[i][0] * f0 + x.x * g0;
-          o[i][1] = o[i][1] * f0 + x.y * g0;
-          o[i][2] = o[i][2] * f1 + y.x * g1;
-          o[i][3] = o[i][3] * f1 + y.y * g1;
+          for (int i = 0; i < HD / 8; ++i) {
+            const int d = i * 8 + (lane & 3) * 2;
+            const float2 x = *reinterpret_cast<const float2*>(bo + row * HD + d);
+            const float2 y = *reinterpret_cast<const float2*>(bo + (row + 8) * HD + d);
+            o[i][0] = o[i][0] * f0 + x.x * g0;
+            o[i][1] = o[i][1] * f0 + x.y * g0;
+            o[i][2] = o[i][2] * f1 + y.x * g1;
+            o[i][3] = o[i][3] * f1 + y.y * g1;
+          }
         }
       }
     }
 
     // ---------------- the pair's output, or this share's partial of it
-    if (warp == 0) {
-      const bool whole = w.tile == 0 && tile_end == w.ntiles;
-      if (whole) {
+    if (W == 1 || warp == 0) {
+      if (use.tile == 0 && use.stop == use.w.ntiles) {
         const float i0 = 1.f / l0, i1 = 1.f / l1;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) {
           const int d = i * 8 + (lane & 3) * 2;
-          uint16_t* out = static_cast<uint16_t*>(c.out) + w.seq * c.o_ss + h0 * c.o_hs + d;
+          uint16_t* out = static_cast<uint16_t*>(c.out) + use.w.seq * c.o_ss + h0 * c.o_hs + d;
           if (row < nh) *reinterpret_cast<uint32_t*>(out + row * c.o_hs) = pack2(o[i][0] * i0, o[i][1] * i0, DT);
           if (row + 8 < nh) *reinterpret_cast<uint32_t*>(out + (row + 8) * c.o_hs) = pack2(o[i][2] * i1, o[i][3] * i1, DT);
         }
         if (c.lse && (lane & 3) == 0) {
-          float* lse = c.lse + (int64_t)w.seq * c.n_heads + h0;
+          float* lse = c.lse + (int64_t)use.w.seq * c.n_heads + h0;
           if (row < nh) lse[row] = (m0 + log2f(l0)) * 0.69314718055994530942f;
           if (row + 8 < nh) lse[row + 8] = (m1 + log2f(l1)) * 0.69314718055994530942f;
         }
       } else {
-        const int64_t box = (int64_t)blockIdx.x * 2 + (at == begin ? 0 : 1);
+        const int64_t box = (int64_t)worker * 2 + (use.tile == 0);
         float* po = p.part_o + box * kRows * HD;
         float* pml = p.part_ml + box * kRows * 2;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) {
           const int d = i * 8 + (lane & 3) * 2;
-          *reinterpret_cast<float2*>(po + row * HD + d) = make_float2(o[i][0], o[i][1]);
-          *reinterpret_cast<float2*>(po + (row + 8) * HD + d) = make_float2(o[i][2], o[i][3]);
+          if (row < nh) *reinterpret_cast<float2*>(po + row * HD + d) = make_float2(o[i][0], o[i][1]);
+          if (row + 8 < nh) *reinterpret_cast<float2*>(po + (row + 8) * HD + d) = make_float2(o[i][2], o[i][3]);
         }
         if ((lane & 3) == 0) {
           pml[row * 2] = m0;
@@ -480,22 +569,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD>::kCtasPerSm) attention_kerne
         }
       }
     }
-    // ---------------- next pair
-    at += tile_end - w.tile;
-    if (at < end) {
-      w.tile = 0;
-      if (++w.unit == p.units) {
-        w.unit = 0;
-        do {
-          ++w.seq;
-          len = keys_of(p, w.seq);
-          w.ntiles = tiles_of(p, len);
-        } while (w.ntiles == 0);
-        start = first_key(p, len);
+    have = next_pair(use);
+  }
+  if (!ok)  // copies still in flight land before the CTA may leave
+    for (; in_flight > 0; --in_flight) {
+      mbar_wait(&full[lost_slot], lost_phase, c.status, 96);
+      if (++lost_slot == ST) {
+        lost_slot = 0;
+        lost_phase ^= 1;
       }
     }
-  }
-  cp_wait<0>();
   grid_release();
 }
 
@@ -509,18 +592,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int per = (c.n_seqs + kJoinThreads - 1) / kJoinThreads;
   const int64_t total = line_total(p, red, per);
   const int b = blockIdx.x + 1;
-  const int ctas = shares(p, total);
-  if (b >= ctas) return;
-  const int64_t border = share_begin(total, ctas, b);
+  const int n = shares(p, total);
+  if (b >= n) return;
+  const int64_t border = share_begin(total, n, b);
   const Where w = locate(p, red, per, border);
-  const int64_t a = w.first, e = a + w.ntiles;
-  if (border == a) return;                             // the border lies between two pairs
-  const int c0 = share_of(total, ctas, a), c1 = share_of(total, ctas, e - 1);
+  const int64_t a = w.first + p.pair_cost, e = a + w.ntiles;  // the pair's tiles on the line
+  if (border <= a) return;                             // the border lies in front of the first tile
+  const int c0 = share_of(total, n, a), c1 = share_of(total, n, e - 1);
   if (b != c0 + 1) return;                             // not the pair's first cut
   const int kvh = w.unit / p.hblocks, hb = w.unit - kvh * p.hblocks;
   const int h0 = kvh * p.group + hb * kRows, nh = min(kRows, p.group - hb * kRows);
   const int r0 = blockIdx.y * kJoinRows;
-  const bool first_is_second = share_begin(total, ctas, c0) < a;  // share c0 began before the pair
   for (int i = threadIdx.x; i < kJoinRows * (HD / 4); i += kJoinThreads) {
     const int r = r0 + i / (HD / 4), d = (i % (HD / 4)) * 4;
     if (r >= nh) break;
@@ -528,12 +610,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int x = c0; x <= c1; ++x) {
-      const int64_t box = (int64_t)x * 2 + (x == c0 && first_is_second ? 1 : 0);
+      const int64_t box = (int64_t)x * 2 + (x == c0);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (box * kRows + r) * 2);
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + (box * kRows + r) * HD + d);
-      const float n = fmaxf(m, ml.x);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - n), g = ml.x == -INFINITY ? 0.f : exp2f(ml.x - n);
-      m = n;
+      const float top = fmaxf(m, ml.x);
+      const float f = m == -INFINITY ? 0.f : ex2(m - top), g = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      m = top;
       l = l * f + ml.y * g;
       o.x = o.x * f + v.x * g;
       o.y = o.y * f + v.y * g;
@@ -548,24 +630,35 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
 }
 
-template <int HD, int DT>
-cudaError_t launch_t(Params& p, cudaStream_t st) {
-  using C = Cfg<HD>;
+template <int HD, int DT, int W>
+cudaError_t launch_w(Params& p, cudaStream_t st) {
+  using C = Cfg<HD, W>;
   int dev = 0;
   cudaGetDevice(&dev);
   static bool attr_done[64] = {false};  // per device
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(attention_kernel<HD, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(attention_kernel<HD, DT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  p.ctas = 148 * C::kCtasPerSm;
+  const int ctas = 148 * C::kCtasPerSm;
+  p.workers = W == 1 ? ctas * kWarps : ctas;
+  p.tile_shift = W == 1 ? 4 : 6;
+  p.pair_cost = W == 1 ? kPairCostWarp : kPairCost;
   p.part_o = static_cast<float*>(p.c.ws);
-  p.part_ml = p.part_o + (int64_t)p.ctas * 2 * kRows * HD;
-  cudaError_t e = launch_dependent(attention_kernel<HD, DT>, dim3(p.ctas), dim3(kThreads), C::kSmem, st, p);
+  p.part_ml = p.part_o + (int64_t)p.workers * 2 * kRows * HD;
+  cudaError_t e = launch_dependent(attention_kernel<HD, DT, W>, dim3(ctas), dim3(kThreads), C::kSmem, st, p);
   if (e != cudaSuccess) return e;
   const int groups = (min(p.group, kRows) + kJoinRows - 1) / kJoinRows;
-  return launch_dependent(join_kernel<HD, DT>, dim3(p.ctas - 1, groups), dim3(kJoinThreads), 0, st, p);
+  return launch_dependent(join_kernel<HD, DT>, dim3(p.workers - 1, groups), dim3(kJoinThreads), 0, st, p);
+}
+
+template <int HD, int DT>
+cudaError_t launch_t(Params& p, cudaStream_t st) {
+  // one pair per warp at least: each warp works alone (heads over 128 wide keep q in shared memory)
+  if constexpr (HD <= 128)
+    if ((int64_t)p.c.n_seqs * p.units >= 148 * Cfg<HD, 1>::kCtasPerSm * kWarps) return launch_w<HD, DT, 1>(p, st);
+  return launch_w<HD, DT, kWarps>(p, st);
 }
 
 template <int DT>
@@ -583,7 +676,7 @@ cudaError_t launch_dt(Params& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t attention_ws_bytes(int head_dim) { return (size_t)kMaxCtas * 2 * kRows * (head_dim + 2) * sizeof(float); }
+size_t attention_ws_bytes(int head_dim) { return (size_t)kMaxWorkers * 2 * kRows * (head_dim + 2) * sizeof(float); }
 
 const char* attention_refuses(int n_seqs, int n_heads, int n_kv, int head_dim, int dt) {
   if (n_seqs < 0 || n_seqs > 65535 || n_heads < 1 || n_heads > 65535 || n_kv < 1 || n_heads % n_kv) return "bad sizes";
@@ -601,6 +694,14 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t st) {
   p.units = c.n_kv * p.hblocks;
   while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
   p.scale_log2 = c.scale * 1.44269504088896340736f;
+  p.box_rows = std::min(c.page_size, kWarpKeys);
+  const uint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.page_size, (uint64_t)c.n_kv, (uint64_t)c.n_pages};
+  const uint64_t strides[3] = {2 * (uint64_t)c.row_stride, 2 * (uint64_t)c.head_stride, 2 * (uint64_t)c.page_stride};
+  const uint32_t box[4] = {64, (uint32_t)p.box_rows, 1, 1};
+  const CUtensorMapDataType dt = c.dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!encode_map_4d(&p.tm_k, dt, c.kc, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map_4d(&p.tm_v, dt, c.vc, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   return c.dt == DT_BF16 ? launch_dt<DT_BF16>(p, st) : launch_dt<DT_F16>(p, st);
 }
 

@@ -148,6 +148,10 @@ cudaError_t launch_quantize_angles(int m, int64_t half_n, const float* theta, in
 bool encode_map_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
 
+// 4-D tiled tensor map (innermost dimension contiguous, byte strides of the other three).
+bool encode_map_4d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                   const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw);
+
 // Records a printf-style message as the thread's last error and returns `st`.
 harp_status set_error(harp_status st, const char* fmt, ...);
 // Per-device status word the kernels report failures into (allocated on first use,

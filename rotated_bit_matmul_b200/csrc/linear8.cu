@@ -2,8 +2,7 @@
 //
 //   y[t][n] = sum_b sx[b][t] sw[n / 128][b] * sum_{k in block b} x8[t][k] w8[n][k]
 //
-// Tensor-core kernel. A tile is 128 weight rows (the MMA's M, one row block of sw) by BT
-// tokens (its N); a K step is one block of 128 columns. Warp 0 streams both operands with TMA
+// Both kernels: one K step is one block of 128 columns. Warp 0 streams the operands with TMA
 // (no multicast) into a ring of 128-byte-swizzled stages, one lane of warp 1 issues
 // tcgen05.mma kind::f8f6f4 (K = 32 each) into tensor memory, and eight warps read every
 // finished block with tcgen05.ld and add it, times its scales, to fp32 sums in registers.
@@ -11,15 +10,19 @@
 // core never holds a sum over more than 128 products, and several accumulators in tensor
 // memory let the MMAs run ahead of the eight warps.
 //
-// The weights are the M side at every batch: one token needs a 128 x 16 tile, in which only
-// the weights' bytes count, and a thread then owns one weight row, so that a warp's store of
-// one token covers 32 consecutive outputs.
+// few_kernel (decode): the weights' bandwidth bounds the work. The weights are the MMA's M side
+// (128 rows, one row block of `sw`) and 16, 32 or 64 tokens its N, so that little but the
+// weights' bytes is loaded; a thread owns one weight row, and a warp's store of one token
+// covers 32 consecutive outputs. The K blocks of a tile are cut over a cluster of up to 8 CTAs;
+// each leaves its fp32 tile in its idle ring, and the cluster adds them in rank order through
+// distributed shared memory (no workspace, no atomics).
 //
-// Few tokens: the weights' bandwidth bounds the work. The K blocks of a tile are cut over a
-// cluster of up to 8 CTAs; each leaves its fp32 tile in its idle ring, and the cluster adds
-// them in rank order through distributed shared memory (no workspace, no atomics).
-// Many tokens: CTAs are persistent and take tiles in an order that keeps the token tiles of
-// one weight tile together in L2.
+// many_kernel (prompts): the tensor cores bound the work. 128 tokens are the M side, so that a
+// thread owns one token and one block of weight rows: all its columns share one scale per K
+// step, and the sums cost one packed FMA per two products' blocks and no shared-memory reads
+// (with the weights as M every column had a scale of its own: two more reads and multiplies
+// per four columns, which the FMA and shared-memory pipes did not have to spare). CTAs are
+// persistent and take tiles in an order that keeps the tiles of one wave close in L2.
 #include "serve.cuh"
 #include "serve.h"
 
@@ -34,6 +37,7 @@ constexpr int kBM = 128;        // weight rows of a tile
 constexpr int kBK = 128;        // columns of a K step = columns that share a scale
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 64 + 32 * kSumWarps;
+constexpr int kManyThreads = 128 + 32 * kSumWarps;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAcc = 8;
 constexpr int kMaxSlots = 32;
@@ -124,6 +128,7 @@ struct Params {
   void* y;
   int yt;
   int64_t ys;
+  int wide;                // rows of y start on 32-byte boundaries
   int* status;
   uint64_t wait_ns;
 };
@@ -131,9 +136,9 @@ struct Params {
 template <int BT>
 struct Cfg {
   static constexpr int kStage = kBM * kBK + BT * kBK;
-  static constexpr int kAcc = BT >= 256 ? 2 : BT >= 128 ? 4 : kMaxAcc;
+  static constexpr int kAcc = kMaxAcc;
   // ring of token scales, one slot per K step: at least stages + accumulators (see the producer)
-  static constexpr int kSlots = BT >= 256 ? 8 : BT >= 128 ? 16 : 32;
+  static constexpr int kSlots = kMaxSlots;
   static constexpr int kCols = kAcc * BT;  // tensor-memory columns: a power of two, at least 32
   static constexpr int kFixed = kSlots * BT * 4 + 1024 /* barriers */ + 1024 /* alignment */;
 };
@@ -158,7 +163,7 @@ __device__ __forceinline__ void tile_at(const Params& p, int i, int& nt, int& tt
 }
 
 template <int BT>
-__global__ void __launch_bounds__(kThreads, 1) linear8_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Params p) {
   using C = Cfg<BT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -356,46 +361,259 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_kernel(const __grid_const
   grid_release();
 }
 
-struct Plan {
-  int bt, splits;
+// ------------------------------------------------------------------ many tokens
+template <int BN>
+struct Many {
+  static constexpr int kStage = kBM * kBK + BN * kBK;
+  static constexpr int kAcc = 512 / BN;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kSlots = kStages + kAcc;  // token scales, as in few_kernel
+  static constexpr int kSmem = kStages * kStage + kSlots * kBM * 4 + 1024 + 1024;
 };
+// Registers: the eight summing warps hold BN / 2 sums and two tcgen05.ld results per thread.
+// The block is launched with 384 x 168; the first warpgroup gives back what the others take
+// (128 x 40 + 256 x 224 <= 384 x 168, checked before every first launch).
+constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 224;
+static_assert(128 * kLowRegs + 256 * kHighRegs <= kManyThreads * kLaunchRegs, "register split");
 
-// Tile width and K split. Few tokens: the narrowest tile that holds them (fewer bytes of
-// scales and operand per stage), cut so that about one CTA per SM streams weights, each over
-// at least 4 K steps. More: the width with the least (waves x width), the wider on a tie.
-Plan choose(int64_t tokens, int64_t n_out, int kblocks) {
-  const int64_t nt = (n_out + kBM - 1) / kBM;
-  Plan best{256, 1};
-  for (int bt : {16, 32, 64, 128})
-    if (tokens <= bt) {
-      best.bt = bt;
-      break;
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Params p) {
+  using C = Many<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int ST = C::kStages, SL = C::kSlots;
+  float* scale_s = reinterpret_cast<float*>(ring + (size_t)ST * C::kStage);  // [SL][128]
+  Bars* bars = reinterpret_cast<Bars*>(scale_s + SL * kBM);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = p.ntiles * p.ttiles, nkb = p.kblocks;
+
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
     }
-  if (tokens > 128) {
-    int64_t cost = INT64_MAX;
-    for (int bt : {256, 128, 64}) {
-      const int64_t tiles = nt * ((tokens + bt - 1) / bt), waves = (tiles + 147) / 148;
-      if (waves * bt < cost) {
-        cost = waves * bt;
-        best.bt = bt;
+    for (int i = 0; i < C::kAcc; ++i) {
+      mbar_init(&bars->accfull[i], 1);
+      mbar_init(&bars->accempty[i], kSumWarps);
+    }
+    for (int i = 0; i < SL; ++i) mbar_init(&bars->scale[i], 1);
+    fence_mbar_init();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(&bars->tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tslot;
+  grid_wait();
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (warp == 0 && lane == 0) {
+      // ---------------- producer
+      tma_prefetch_desc(&p.tm_w);
+      tma_prefetch_desc(&p.tm_x);
+      int k = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+        int nt, tt;
+        tile_at(p, i, nt, tt);
+        const uint32_t sbytes = (uint32_t)(min(kBM, (p.tokens - tt * kBM + 3) & ~3) * 4);
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int slot = k % ST;
+          if (k >= ST && !mbar_wait_sleep(&bars->empty[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + (size_t)slot * C::kStage;
+          mbar_arrive_expect_tx(&bars->full[slot], C::kStage);
+          tma_load_2d(st, &p.tm_x, &bars->full[slot], kb * kBK, tt * kBM);
+          tma_load_2d(st + kBM * kBK, &p.tm_w, &bars->full[slot], kb * kBK, nt * BN);
+          // free since step k - ST's MMA was issued (see few_kernel)
+          uint64_t* sb = &bars->scale[k % SL];
+          mbar_arrive_expect_tx(sb, sbytes);
+          bulk_g2s(scale_s + (k % SL) * kBM, p.sx + (int64_t)kb * p.sx_ld + (int64_t)tt * kBM, sbytes, sb);
+        }
+      }
+      for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->full[q % ST], (q / ST) & 1, p.status, 101, p.wait_ns);
+      for (int q = max(0, k - SL); q < k; ++q) mbar_wait(&bars->scale[q % SL], (q / SL) & 1, p.status, 102, p.wait_ns);
+    } else if (warp == 1 && lane == 0) {
+      // ---------------- MMA issuer
+      const uint32_t idesc = idesc_e4m3(kBM, BN);
+      int k = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int slot = k % ST, b = k % C::kAcc;
+          if (k >= C::kAcc && !mbar_wait(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns)) ok = false;
+          if (ok && !mbar_wait(&bars->full[slot], (k / ST) & 1, p.status, 104, p.wait_ns)) ok = false;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + (size_t)slot * C::kStage), w = a + kBM * kBK;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_e4m3(tmem + b * BN, sw128_desc(a + 32 * kk), sw128_desc(w + 32 * kk), idesc, kk != 0);
+          mma_commit(&bars->empty[slot]);
+          mma_commit(&bars->accfull[b]);
+        }
+      for (int q = max(0, k - C::kAcc); q < k; ++q)
+        mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- scaled sums: thread = token, half the tile's weight rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
+    constexpr int HC = BN / 2, NQ = HC / 32;
+    const int quad = warp & 3, half = (warp - 4) >> 2, c0 = half * HC;
+    const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + c0;
+    int k = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      int nt, tt;
+      tile_at(p, i, nt, tt);
+      uint64_t acc[HC / 2];
+#pragma unroll
+      for (int j = 0; j < HC / 2; ++j) acc[j] = 0ull;
+      // this half's block of weight rows (the last tile's second half may lie outside)
+      const int nb = min((nt * BN + c0) / kBK, (p.n_out - 1) / kBK);
+      const float* swp = p.sw + (int64_t)nb * nkb;
+      float sw_l = 0.f;  // lane j: weight scale of K step 32 * (kb / 32) + j
+      for (int kb = 0; kb < nkb; ++kb, ++k) {
+        if ((kb & 31) == 0) sw_l = kb + lane < nkb ? __ldg(swp + kb + lane) : 0.f;
+        const int b = k % C::kAcc;
+        ok = mbar_wait(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
+             mbar_wait(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const float s = scale_s[(k % SL) * kBM + quad * 32 + lane] * __shfl_sync(0xffffffffu, sw_l, kb & 31);
+        const uint64_t s2 = f32x2(s, s);
+        tc_fence_after();
+        // one tcgen05.ld in flight while the one before it is summed
+        uint32_t r[2][32];
+        tmem_ld32(tl + b * BN, r[0]);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          tmem_wait();
+          if (q + 1 < NQ) {
+            tmem_ld32(tl + b * BN + (q + 1) * 32, r[(q + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->accempty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            acc[(q * 32 + j) / 2] = fma2((uint64_t)r[q & 1][j] | ((uint64_t)r[q & 1][j + 1] << 32), s2, acc[(q * 32 + j) / 2]);
+        }
+      }
+      const int64_t t = (int64_t)tt * kBM + quad * 32 + lane;
+      const int n0 = nt * BN + c0, valid = min(HC, p.n_out - n0);
+      if (t < p.tokens && valid > 0 && ok) {
+        auto column = [&](int j) { return __uint_as_float((uint32_t)(j & 1 ? acc[j / 2] >> 32 : acc[j / 2])); };
+        if (p.yt == DT_F32) {
+          float* y = static_cast<float*>(p.y) + t * p.ys + n0;
+          if (p.wide && valid == HC) {
+#pragma unroll
+            for (int j = 0; j < HC; j += 8) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(column(j + e));
+              st_global_32(y + j, v);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < HC; ++j)
+              if (j < valid) y[j] = column(j);
+          }
+        } else {
+          uint16_t* y = static_cast<uint16_t*>(p.y) + t * p.ys + n0;
+          if (p.wide && valid == HC) {
+#pragma unroll
+            for (int j = 0; j < HC; j += 16) {
+              uint32_t v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = pack2(column(j + 2 * e), column(j + 2 * e + 1), p.yt);
+              st_global_32(y + j, v);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < HC; j += 2) {
+              const uint32_t v = pack2(column(j), column(j + 1), p.yt);
+              if (j < valid) y[j] = (uint16_t)v;
+              if (j + 1 < valid) y[j + 1] = (uint16_t)(v >> 16);
+            }
+          }
+        }
       }
     }
   }
-  const int64_t tiles = nt * ((tokens + best.bt - 1) / best.bt);
-  if (best.bt <= 64)
-    while (best.splits < 8 && tiles * best.splits * 2 <= 160 && kblocks / (best.splits * 2) >= 4) best.splits *= 2;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  grid_release();
+}
+
+// ------------------------------------------------------------------ choice and launch
+struct Plan {
+  bool many;
+  int width, splits;  // tokens (few) or weight rows (many) of a tile's N side; CTAs per tile
+};
+
+// Up to 128 tokens, or too few 128 x 128 tiles to fill the GPU: few_kernel with the narrowest
+// tile that holds the tokens (64 at most), cut over K so that about one CTA per SM streams
+// weights, each over at least 4 K steps. Else many_kernel, 256 wide unless 128 takes fewer
+// waves x width.
+Plan choose(int64_t tokens, int64_t n_out, int kblocks) {
+  auto tiles = [&](int64_t w, int64_t t) { return ((n_out + w - 1) / w) * ((tokens + t - 1) / t); };
+  if (tokens > 128 && tiles(128, 128) >= 100) {
+    const int64_t w256 = (tiles(256, 128) + 147) / 148 * 256, w128 = (tiles(128, 128) + 147) / 148 * 128;
+    return Plan{true, w128 < w256 ? 128 : 256, 1};
+  }
+  Plan best{false, tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, 1};
+  const int64_t n = tiles(kBM, best.width);
+  while (best.splits < 8 && n * best.splits * 2 <= 160 && kblocks / (best.splits * 2) >= 4) best.splits *= 2;
   return best;
 }
 
+template <int BN>
+cudaError_t launch_many(Params& p, cudaStream_t st) {
+  using C = Many<BN>;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool ready[64] = {false};  // per device
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    cudaFuncAttributes a{};
+    cudaError_t e = cudaFuncGetAttributes(&a, many_kernel<BN>);
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc would wait for ever for registers that the launch did not have
+    if (a.numRegs * kManyThreads < 128 * kLowRegs + 256 * kHighRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(many_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  return launch_dependent(many_kernel<BN>, dim3((unsigned)std::min(p.ntiles * p.ttiles, 148)), dim3(kManyThreads), C::kSmem, st, p);
+}
+
 template <int BT>
-cudaError_t launch_t(Params& p, cudaStream_t st) {
+cudaError_t launch_few(Params& p, cudaStream_t st) {
   using C = Cfg<BT>;
   int dev = 0, optin = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   static bool attr_done[64] = {false};  // per device
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(linear8_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+    const cudaError_t e = cudaFuncSetAttribute(few_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
@@ -420,7 +638,7 @@ cudaError_t launch_t(Params& p, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear8_kernel<BT>, p);
+  return cudaLaunchKernelEx(&cfg, few_kernel<BT>, p);
 }
 
 }  // namespace
@@ -430,7 +648,7 @@ cudaError_t launch_t(Params& p, cudaStream_t st) {
 using namespace harp;
 
 struct harp_layer8_s {
-  CUtensorMap tm_w;
+  CUtensorMap tm_w, tm_w256;  // boxes of 128 and 256 rows
   int64_t n_out, n_in;
   const float* sw;
   int device;
@@ -457,8 +675,11 @@ harp_status harp_create_layer8(harp_layer8* out, int64_t n_in, int64_t n_out, co
   L->n_out = n_out;
   L->sw = scale;
   L->device = dev;
-  if (!encode_map_2d(&L->tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, (uint64_t)n_in, (uint64_t)n_out, (uint64_t)row_stride,
-                     l8::kBK, l8::kBM, CU_TENSOR_MAP_SWIZZLE_128B)) {
+  auto map = [&](CUtensorMap* tm, uint32_t rows) {
+    return encode_map_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, (uint64_t)n_in, (uint64_t)n_out, (uint64_t)row_stride,
+                         l8::kBK, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!map(&L->tm_w, l8::kBM) || !map(&L->tm_w256, 2 * l8::kBM)) {
     delete L;
     return set_error(HARP_ERR_CUDA, "create_layer8: cuTensorMapEncodeTiled failed");
   }
@@ -488,13 +709,13 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
   l8::Params p{};
   harp_status s = device_status_for_kernels(&p.status);
   if (s != HARP_OK) return s;
-  p.tm_w = L->tm_w;
   p.n_out = (int)L->n_out;
   p.tokens = (int)tokens;
   p.kblocks = (int)((L->n_in + l8::kBK - 1) / l8::kBK);
-  p.ntiles = (int)((L->n_out + l8::kBM - 1) / l8::kBM);
   const l8::Plan plan = l8::choose(tokens, L->n_out, p.kblocks);
-  p.ttiles = (int)((tokens + plan.bt - 1) / plan.bt);
+  const int nw = plan.many ? plan.width : l8::kBM, tw = plan.many ? l8::kBM : plan.width;  // weight rows, tokens of a tile
+  p.ntiles = (int)((L->n_out + nw - 1) / nw);
+  p.ttiles = (int)((tokens + tw - 1) / tw);
   p.splits = plan.splits;
   p.sx = x_scale;
   p.sx_ld = scale_ld;
@@ -502,19 +723,16 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
   p.y = y;
   p.yt = yt;
   p.ys = y_stride;
+  p.wide = aligned_to(y, 32) && (y_stride * dtype_bytes(yt)) % 32 == 0;
   p.wait_ns = test_hooks().wait_ns;
+  p.tm_w = nw == 256 ? L->tm_w256 : L->tm_w;
   if (!encode_map_2d(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)L->n_in, (uint64_t)tokens, (uint64_t)x_stride,
-                     l8::kBK, (uint32_t)plan.bt, CU_TENSOR_MAP_SWIZZLE_128B))
+                     l8::kBK, (uint32_t)tw, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(HARP_ERR_CUDA, "linear8_fwd: cuTensorMapEncodeTiled failed");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (plan.bt) {
-    case 16: e = l8::launch_t<16>(p, st); break;
-    case 32: e = l8::launch_t<32>(p, st); break;
-    case 64: e = l8::launch_t<64>(p, st); break;
-    case 128: e = l8::launch_t<128>(p, st); break;
-    case 256: e = l8::launch_t<256>(p, st); break;
-  }
+  cudaError_t e;
+  if (plan.many) e = plan.width == 256 ? l8::launch_many<256>(p, st) : l8::launch_many<128>(p, st);
+  else e = plan.width == 16 ? l8::launch_few<16>(p, st) : plan.width == 32 ? l8::launch_few<32>(p, st) : l8::launch_few<64>(p, st);
   return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "linear8 launch: %s", cudaGetErrorString(e));
 }
 

@@ -7,8 +7,8 @@
 // One pass: a row's values are loaded once and stay in registers between the sum of squares
 // and the output, so the kernel moves what the formula needs and no more. The sum of squares
 // is fp32 (a thread's few values, then a fixed tree), the mean and its root are taken in
-// fp64 (once per row), and q is an IEEE division, so that a code differs from the exact one
-// only where y / s lies within fp32 rounding of the border between two codes.
+// fp64 (once per row), and y / s is good to 1.5 units, so that a code differs from the exact
+// one only where y / s lies within fp32 rounding of the border between two codes.
 //
 // Two mappings of a row onto threads:
 //   * rows that start on 16-byte boundaries: a thread holds 8 consecutive columns per step
@@ -18,6 +18,8 @@
 #include "serve.cuh"
 
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 namespace harp {
 namespace {
@@ -58,6 +60,19 @@ __device__ __forceinline__ float block_scale(float amax) {
   return s == 0.f ? 1.f : s;
 }
 
+// v / s: times 1 / s (rounded twice, within 1.5 units), divided where 1 / s would overflow
+template <int N>
+__device__ __forceinline__ void over_scale(const float (&v)[N], float s, float (&d)[N]) {
+  if (s >= 0x1p-120f || !(s == s)) {
+    const float r = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = v[i] * r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = v[i] / s;
+  }
+}
+
 // sum over the blockDim.x threads of this row (a fixed tree, the same in every thread)
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
@@ -77,9 +92,14 @@ __device__ __forceinline__ float inv_rms(float sum, int n, float eps) {
   return (float)(1.0 / sqrt((double)sum / n + (double)eps));
 }
 
-// blockDim = (threads per row, rows per CTA); more than one row per CTA only with 32 threads
-template <int STEPS, bool Q8>
-__global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ NormParams p) {
+// blockDim = (threads per row, rows per CTA); more than one row per CTA only with 32 threads.
+// XT: type of x; RT: type of the residual, or kNone. The types are fixed at compile time so
+// that all of a thread's loads are issued together; run-time branches on them put one wait
+// behind each (8192 x 8192 bf16: 163 us).
+constexpr int kNone = -1;
+
+template <int XT, int RT, int STEPS, bool Q8>
+__global__ void __launch_bounds__(STEPS == 1 ? 1024 : 512) norm_vec_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[32];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int tx = threadIdx.x, T = blockDim.x;
@@ -94,18 +114,18 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ 
     for (int k = 0; k < STEPS; ++k) {
       const int c = (k * T + tx) * 8;
       if (c + 8 <= n) {
-        rx[k] = raw_load8(p.x, xo + c, p.xt);
-        if (p.r) rr[k] = raw_load8(p.r, ro + c, p.rt);
+        rx[k] = raw_load8(p.x, xo + c, XT);
+        if (RT != kNone) rr[k] = raw_load8(p.r, ro + c, RT);
       }
     }
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
       const int c = (k * T + tx) * 8;
       if (c + 8 <= n) {
-        raw_unpack8(rx[k], p.xt, v[k]);
-        if (p.r) {
+        raw_unpack8(rx[k], XT, v[k]);
+        if (RT != kNone) {
           float t[8];
-          raw_unpack8(rr[k], p.rt, t);
+          raw_unpack8(rr[k], RT, t);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[k][i] += t[i];
         }
@@ -113,19 +133,19 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           v[k][i] = 0.f;
-          if (c + i < n) v[k][i] = load_act(p.x, xo + c + i, p.xt) + (p.r ? load_act(p.r, ro + c + i, p.rt) : 0.f);
+          if (c + i < n) v[k][i] = load_act(p.x, xo + c + i, XT) + (RT != kNone ? load_act(p.r, ro + c + i, RT) : 0.f);
         }
       }
     }
   }
-  if (p.h) {
+  if (RT != kNone && p.h) {
     const int64_t ho = row * p.hs;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
       const int c = (k * T + tx) * 8;
-      if (c + 8 <= n) store8(p.h, ho + c, p.rt, v[k]);
+      if (c + 8 <= n) store8(p.h, ho + c, RT, v[k]);
       else
-        for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.h, ho + c + i, p.rt, v[k][i]);
+        for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.h, ho + c + i, RT, v[k][i]);
     }
   }
   if (p.norm) {
@@ -136,22 +156,28 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ 
       for (int i = 0; i < 8; ++i) s = fmaf(v[k][i], v[k][i], s);
     const float inv = inv_rms(row_sum(s, red), n, p.eps);
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-      const int c = (k * T + tx) * 8;
+    for (int k = 0; k < STEPS; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[k][i] *= inv;
-      if (p.w) {
-        if (c + 8 <= n) {
-          float t[8];
-          raw_unpack8(raw_load8(p.w, c, p.wt), p.wt, t);
+    if (p.w) {
+      auto weigh = [&](int wt) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] *= t[i];
-        } else {
+        for (int k = 0; k < STEPS; ++k) {
+          const int c = (k * T + tx) * 8;
+          if (c + 8 <= n) {
+            float t[8];
+            raw_unpack8(raw_load8(p.w, c, wt), wt, t);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < n) v[k][i] *= load_act(p.w, c + i, p.wt);
+            for (int i = 0; i < 8; ++i) v[k][i] *= t[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c + i < n) v[k][i] *= load_act(p.w, c + i, wt);
+          }
         }
-      }
+      };
+      if (p.wt == XT) weigh(XT);  // the usual case without a branch per step
+      else weigh(p.wt);
     }
   }
   const int64_t yo = row * p.ys;
@@ -168,11 +194,13 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ 
       if (c < n) {
         if ((tx & 15) == 0) p.scale[(int64_t)(c / kBlk) * p.scale_ld + row] = s;
         uint8_t* q = static_cast<uint8_t*>(p.y) + yo + c;
+        float d[8];
+        over_scale(v[k], s, d);
         uint32_t w[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[k][4 * j] / s, v[k][4 * j + 1] / s), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[k][4 * j + 2] / s, v[k][4 * j + 3] / s), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(d[4 * j], d[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(d[4 * j + 2], d[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
           w[j] = lo | (hi << 16);
         }
         if (c + 8 <= n) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
@@ -188,7 +216,10 @@ __global__ void __launch_bounds__(1024) norm_vec_kernel(const __grid_constant__ 
 }
 
 // the same for rows at any alignment: a warp per block of 128 columns and step
-template <int STEPS, bool Q8>
+// (kAny: a residual in a 16-bit type that is not x's, or in one with an fp32 x, told at run time)
+constexpr int kAny = -2;
+
+template <int XT, int RT, int STEPS, bool Q8>
 __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[32];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -203,25 +234,25 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = (k * W + warp) * kBlk + i * 32 + lane;
-      v[k][i] = c < n ? load_act(p.x, xo + c, p.xt) : 0.f;
+      v[k][i] = c < n ? load_act(p.x, xo + c, XT) : 0.f;
     }
-  if (p.r) {
+  if (RT != kNone) {
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = (k * W + warp) * kBlk + i * 32 + lane;
-        if (c < n) v[k][i] += load_act(p.r, ro + c, p.rt);
+        if (c < n) v[k][i] += load_act(p.r, ro + c, RT == kAny ? p.rt : RT);
       }
   }
-  if (p.h) {
+  if (RT != kNone && p.h) {
     const int64_t ho = row * p.hs;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = (k * W + warp) * kBlk + i * 32 + lane;
-        if (c < n) store_act(p.h, ho + c, p.rt, v[k][i]);
+        if (c < n) store_act(p.h, ho + c, RT == kAny ? p.rt : RT, v[k][i]);
       }
   }
   if (p.norm) {
@@ -231,14 +262,18 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fmaf(v[k][i], v[k][i], s);
     const float inv = inv_rms(row_sum(s, red), n, p.eps);
+    auto weigh = [&](int wt) {
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k)
+      for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (k * W + warp) * kBlk + i * 32 + lane;
-        v[k][i] *= inv;
-        if (p.w && c < n) v[k][i] *= load_act(p.w, c, p.wt);
-      }
+        for (int i = 0; i < 4; ++i) {
+          const int c = (k * W + warp) * kBlk + i * 32 + lane;
+          v[k][i] *= inv;
+          if (p.w && c < n) v[k][i] *= load_act(p.w, c, wt);
+        }
+    };
+    if (p.wt == XT) weigh(XT);
+    else weigh(p.wt);
   }
   const int64_t yo = row * p.ys;
 #pragma unroll
@@ -255,11 +290,13 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
       s = block_scale(amax);
       if (lane == 0) p.scale[(int64_t)(c0 / kBlk) * p.scale_ld + row] = s;
     }
+    float d[4];
+    if (Q8) over_scale(v[k], s, d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = c0 + i * 32 + lane;
       if (c >= n) continue;
-      if (Q8) static_cast<uint8_t*>(p.y)[yo + c] = __nv_cvt_float_to_fp8(v[k][i] / s, __NV_SATFINITE, __NV_E4M3);
+      if (Q8) static_cast<uint8_t*>(p.y)[yo + c] = __nv_cvt_float_to_fp8(d[i], __NV_SATFINITE, __NV_E4M3);
       else store_act(p.y, yo + c, p.yt, v[k][i]);
     }
   }
@@ -296,10 +333,12 @@ __global__ void __launch_bounds__(256) weights_q8_kernel(const void* w, int wt, 
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int64_t r = r0 + tr + 16 * k;
+    float d[8];
+    over_scale(v[k], s, d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t c = c0 + tc + i;
-      if (r < n_out && c < n_in) q[r * qs + c] = __nv_cvt_float_to_fp8(v[k][i] / s, __NV_SATFINITE, __NV_E4M3);
+      if (r < n_out && c < n_in) q[r * qs + c] = __nv_cvt_float_to_fp8(d[i], __NV_SATFINITE, __NV_E4M3);
     }
   }
 }
@@ -309,24 +348,45 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
   auto on16 = [&](const void* ptr, int64_t stride, int bytes) {
     return !ptr || p.rows == 1 || (stride * bytes) % 16 == 0;
   };
-  const bool vec = on16(p.x, p.xs, dtype_bytes(p.xt)) && on16(p.r, p.rs, dtype_bytes(p.rt)) &&
+  // (kAny residuals are left to the general kernel)
+  const bool vec = (!p.r || p.rt == p.xt || p.rt == DT_F32) && on16(p.x, p.xs, dtype_bytes(p.xt)) && on16(p.r, p.rs, dtype_bytes(p.rt)) &&
                    on16(p.h, p.hs, dtype_bytes(p.rt)) && on16(p.y, p.ys, Q8 ? 1 : dtype_bytes(p.yt));
   const int per = vec ? 256 : kBlk;             // columns a warp covers per step
   const int warps = (p.n + per - 1) / per;      // with one step per thread
+  // Few rows: as many threads as the row has work for, for latency. Many: up to 4 steps per
+  // thread, so that an SM holds several rows and one row's sum hides behind another's loads
+  // (8192 x 8192 bf16 with a residual: one step 179 us).
   int steps = 1;
-  while ((warps + steps - 1) / steps > 32) steps *= 2;
+  const int most = 4;
+  if (p.rows > 2 * 148)
+    while (steps < most && warps > 4 * steps) steps *= 2;
+  while ((warps + steps - 1) / steps > (steps == 1 || !vec ? 32 : 16)) steps *= 2;
   const int tpr = 32 * ((warps + steps - 1) / steps);
   const int rpb = tpr == 32 ? 4 : 1;
   const dim3 grid((unsigned)((p.rows + rpb - 1) / rpb)), block(tpr, rpb);
-  if (vec) {
-    if (steps == 1) return launch_dependent(norm_vec_kernel<1, Q8>, grid, block, 0, st, p);
-    if (steps == 2) return launch_dependent(norm_vec_kernel<2, Q8>, grid, block, 0, st, p);
-    return launch_dependent(norm_vec_kernel<4, Q8>, grid, block, 0, st, p);
-  }
-  if (steps == 1) return launch_dependent(norm_any_kernel<1, Q8>, grid, block, 0, st, p);
-  if (steps == 2) return launch_dependent(norm_any_kernel<2, Q8>, grid, block, 0, st, p);
-  if (steps == 4) return launch_dependent(norm_any_kernel<4, Q8>, grid, block, 0, st, p);
-  return launch_dependent(norm_any_kernel<8, Q8>, grid, block, 0, st, p);
+  auto go = [&](auto xt, auto rt) {
+    constexpr int X = decltype(xt)::value, R = decltype(rt)::value;
+    if constexpr (R != kAny)
+      if (vec) {
+        if (steps == 1) return launch_dependent(norm_vec_kernel<X, R, 1, Q8>, grid, block, 0, st, p);
+        if (steps == 2) return launch_dependent(norm_vec_kernel<X, R, 2, Q8>, grid, block, 0, st, p);
+        if (steps == 4) return launch_dependent(norm_vec_kernel<X, R, 4, Q8>, grid, block, 0, st, p);
+        return launch_dependent(norm_vec_kernel<X, R, 8, Q8>, grid, block, 0, st, p);
+      }
+    if (steps == 1) return launch_dependent(norm_any_kernel<X, R, 1, Q8>, grid, block, 0, st, p);
+    if (steps == 2) return launch_dependent(norm_any_kernel<X, R, 2, Q8>, grid, block, 0, st, p);
+    if (steps == 4) return launch_dependent(norm_any_kernel<X, R, 4, Q8>, grid, block, 0, st, p);
+    return launch_dependent(norm_any_kernel<X, R, 8, Q8>, grid, block, 0, st, p);
+  };
+  auto with = [&](auto xt) {
+    if (!p.r) return go(xt, std::integral_constant<int, kNone>{});
+    if (p.rt == p.xt) return go(xt, xt);
+    if (p.rt == DT_F32) return go(xt, std::integral_constant<int, DT_F32>{});
+    return go(xt, std::integral_constant<int, kAny>{});
+  };
+  if (p.xt == DT_F32) return with(std::integral_constant<int, DT_F32>{});
+  if (p.xt == DT_BF16) return with(std::integral_constant<int, DT_BF16>{});
+  return with(std::integral_constant<int, DT_F16>{});
 }
 
 // the arguments shared by the three entry points over rows

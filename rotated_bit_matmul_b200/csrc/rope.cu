@@ -173,7 +173,7 @@ harp_status check_cache(const char* who, const harp_kv_cache* c) {
   if (c->page_size < 1 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
     return set_error(HARP_ERR_INVALID_ARG, "%s: page_size=%d must be a power of two, at most 4096", who, c->page_size);
   if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || c->page_stride % 8 || c->head_stride % 8 || c->row_stride % 8 ||
-      c->row_stride < c->head_dim || c->head_stride < 0 || c->page_stride < 0)
+      c->row_stride < c->head_dim || c->head_stride < 8 || c->page_stride < 8)
     return set_error(HARP_ERR_INVALID_ARG, "%s: cache rows must lie on 16-byte boundaries, row_stride at least head_dim", who);
   return HARP_OK;
 }
