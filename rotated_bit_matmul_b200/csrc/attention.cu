@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
 
     for (int tile = use.tile; tile < use.stop; ++tile) {
       if (ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], phase, c.status, 95));
+        ok = mbar_wait_warp(&full[slot], phase, c.status, 95, 1000000000ull);
         if (ok) {
           --in_flight;
         } else {  // reported: ask for nothing more and run to the end

@@ -37,7 +37,6 @@ constexpr int kBM = 128;        // weight rows of a tile
 constexpr int kBK = 128;        // columns of a K step = columns that share a scale
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 64 + 32 * kSumWarps;
-constexpr int kManyThreads = 128 + 32 * kSumWarps;
 constexpr int kMaxStages = 12;
 constexpr int kMaxAcc = 8;
 constexpr int kMaxSlots = 32;
@@ -61,6 +60,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t ad, uint64_t bd, u
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
       : "memory");
+}
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -136,9 +141,10 @@ struct Params {
 template <int BT>
 struct Cfg {
   static constexpr int kStage = kBM * kBK + BT * kBK;
-  static constexpr int kAcc = kMaxAcc;
+  static constexpr int kAcc = BT >= 64 ? 4 : kMaxAcc;
+  static constexpr int kPerSm = 2;  // CTAs per SM (256 of its 512 tensor-memory columns each at most)
   // ring of token scales, one slot per K step: at least stages + accumulators (see the producer)
-  static constexpr int kSlots = kMaxSlots;
+  static constexpr int kSlots = 16;
   static constexpr int kCols = kAcc * BT;  // tensor-memory columns: a power of two, at least 32
   static constexpr int kFixed = kSlots * BT * 4 + 1024 /* barriers */ + 1024 /* alignment */;
 };
@@ -163,7 +169,7 @@ __device__ __forceinline__ void tile_at(const Params& p, int i, int& nt, int& tt
 }
 
 template <int BT>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __grid_constant__ Params p) {
   using C = Cfg<BT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -210,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const uint32_t sbytes = (uint32_t)(min(BT, (p.tokens - tt * BT + 3) & ~3) * 4);
         for (int kb = kb0; kb < kb1; ++kb, ++k) {
           const int slot = k % ST;
-          if (k >= ST && !mbar_wait_sleep(&bars->empty[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
+          if (k >= ST && !mbar_wait_lane(&bars->empty[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -241,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int slot = k % ST, b = k % C::kAcc;
-          if (k >= C::kAcc && !mbar_wait_sleep(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns)) ok = false;
-          if (ok && !mbar_wait_sleep(&bars->full[slot], (k / ST) & 1, p.status, 104, p.wait_ns)) ok = false;
+          if (k >= C::kAcc && !mbar_wait_lane(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns)) ok = false;
+          if (ok && !mbar_wait_lane(&bars->full[slot], (k / ST) & 1, p.status, 104, p.wait_ns)) ok = false;
           if (!ok) break;
           tc_fence_after();
           const uint32_t a = smem_u32(ring + (size_t)slot * C::kStage), x = a + kBM * kBK;
@@ -278,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const int b = k % C::kAcc;
         int got = 1;
         if (lane == 0)
-          got = mbar_wait_sleep(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
-                mbar_wait_sleep(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
+          got = mbar_wait_lane(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
+                mbar_wait_lane(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
         if (!__shfl_sync(0xffffffffu, got, 0)) {
           ok = false;
           break;
@@ -362,19 +368,24 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ many tokens
+// Sum warps: four (the quarters of the 128 tokens) for every 64 weight rows, so that a thread
+// holds 64 sums and the 64 values of a step's block at once: one tcgen05.ld latency per step.
+// Half the warps with 128 sums each took four latencies and 1.47 ms for 4096 x 8192 x 28672.
 template <int BN>
 struct Many {
+  static constexpr int kSums = BN / 64 * 4;
+  static constexpr int kThr = 128 + 32 * kSums;
   static constexpr int kStage = kBM * kBK + BN * kBK;
-  static constexpr int kAcc = 512 / BN;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kSlots = kStages + kAcc;  // token scales, as in few_kernel
-  static constexpr int kSmem = kStages * kStage + kSlots * kBM * 4 + 1024 + 1024;
+  static constexpr int kAcc = BN == 192 ? 2 : 4;
+  static constexpr int kAccCols = 512 / kAcc;  // tensor-memory columns from one accumulator to the next
+  static constexpr int kStages = BN == 192 ? 5 : 6;
+  static constexpr int kSmem = kStages * kStage + 1024 /* barriers */ + 1024 /* alignment */;
+  // Registers: a launch of 512 threads has 128 each; the first warpgroup gives back what the
+  // others take (setmaxnreg), 128 x kLow + (kThr - 128) x kHigh <= kThr x kLaunch
+  static constexpr bool kSplitRegs = BN == 192;
+  static constexpr int kLaunch = 128, kLow = 40, kHigh = 152;
+  static_assert(!kSplitRegs || 128 * kLow + (kThr - 128) * kHigh <= kThr * kLaunch, "register split");
 };
-// Registers: the eight summing warps hold BN / 2 sums and two tcgen05.ld results per thread.
-// The block is launched with 384 x 168; the first warpgroup gives back what the others take
-// (128 x 40 + 256 x 224 <= 384 x 168, checked before every first launch).
-constexpr int kLaunchRegs = 168, kLowRegs = 40, kHighRegs = 224;
-static_assert(128 * kLowRegs + 256 * kHighRegs <= kManyThreads * kLaunchRegs, "register split");
 
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -383,13 +394,12 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
 }
 
 template <int BN>
-__global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_constant__ Params p) {
   using C = Many<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int ST = C::kStages, SL = C::kSlots;
-  float* scale_s = reinterpret_cast<float*>(ring + (size_t)ST * C::kStage);  // [SL][128]
-  Bars* bars = reinterpret_cast<Bars*>(scale_s + SL * kBM);
+  constexpr int ST = C::kStages;
+  Bars* bars = reinterpret_cast<Bars*>(ring + (size_t)ST * C::kStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = p.ntiles * p.ttiles, nkb = p.kblocks;
 
@@ -400,9 +410,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
     }
     for (int i = 0; i < C::kAcc; ++i) {
       mbar_init(&bars->accfull[i], 1);
-      mbar_init(&bars->accempty[i], kSumWarps);
+      mbar_init(&bars->accempty[i], C::kSums);
     }
-    for (int i = 0; i < SL; ++i) mbar_init(&bars->scale[i], 1);
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -414,20 +423,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
   grid_wait();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLow));
     if (warp == 0 && lane == 0) {
       // ---------------- producer
       tma_prefetch_desc(&p.tm_w);
       tma_prefetch_desc(&p.tm_x);
-      int k = 0;
+      int k = 0, slot = 0;
+      uint32_t turn = 1;  // parity of the phase before the slot's next one
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
         int nt, tt;
         tile_at(p, i, nt, tt);
-        const uint32_t sbytes = (uint32_t)(min(kBM, (p.tokens - tt * kBM + 3) & ~3) * 4);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          const int slot = k % ST;
-          if (k >= ST && !mbar_wait_sleep(&bars->empty[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
+          if (k >= ST && !mbar_wait_lane(&bars->empty[slot], turn, p.status, 100, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -435,42 +443,56 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
           mbar_arrive_expect_tx(&bars->full[slot], C::kStage);
           tma_load_2d(st, &p.tm_x, &bars->full[slot], kb * kBK, tt * kBM);
           tma_load_2d(st + kBM * kBK, &p.tm_w, &bars->full[slot], kb * kBK, nt * BN);
-          // free since step k - ST's MMA was issued (see few_kernel)
-          uint64_t* sb = &bars->scale[k % SL];
-          mbar_arrive_expect_tx(sb, sbytes);
-          bulk_g2s(scale_s + (k % SL) * kBM, p.sx + (int64_t)kb * p.sx_ld + (int64_t)tt * kBM, sbytes, sb);
+          if (++slot == ST) {
+            slot = 0;
+            turn ^= 1;
+          }
         }
       }
       for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->full[q % ST], (q / ST) & 1, p.status, 101, p.wait_ns);
-      for (int q = max(0, k - SL); q < k; ++q) mbar_wait(&bars->scale[q % SL], (q / SL) & 1, p.status, 102, p.wait_ns);
-    } else if (warp == 1 && lane == 0) {
-      // ---------------- MMA issuer
+    } else if (warp == 1) {
+      // ---------------- MMA issuer: the whole warp walks the steps, so that descriptors and
+      // addresses stay warp-uniform, and one lane issues
       const uint32_t idesc = idesc_e4m3(kBM, BN);
-      int k = 0;
+      const uint64_t a0 = sw128_desc(smem_u32(ring)), w0 = sw128_desc(smem_u32(ring) + kBM * kBK);
+      const bool leader = elect_lane();
+      int k = 0, slot = 0;
+      uint32_t turn = 0;
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          const int slot = k % ST, b = k % C::kAcc;
-          if (k >= C::kAcc && !mbar_wait(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns)) ok = false;
-          if (ok && !mbar_wait(&bars->full[slot], (k / ST) & 1, p.status, 104, p.wait_ns)) ok = false;
-          if (!ok) break;
+          const int b = k % C::kAcc;
+          if (k >= C::kAcc) ok = mbar_wait_spin(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns);
+          ok = ok && mbar_wait_spin(&bars->full[slot], turn, p.status, 104, p.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          const uint32_t a = smem_u32(ring + (size_t)slot * C::kStage), w = a + kBM * kBK;
+          const uint64_t off = (uint64_t)(slot * (C::kStage >> 4));
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_e4m3(tmem + b * BN, sw128_desc(a + 32 * kk), sw128_desc(w + 32 * kk), idesc, kk != 0);
-          mma_commit(&bars->empty[slot]);
-          mma_commit(&bars->accfull[b]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_e4m3(tmem + b * C::kAccCols, a0 + off + 2 * kk, w0 + off + 2 * kk, idesc, kk != 0);
+            mma_commit(&bars->accfull[b]);
+            mma_commit(&bars->empty[slot]);
+          }
+          __syncwarp();
+          if (++slot == ST) {
+            slot = 0;
+            turn ^= 1;
+          }
         }
-      for (int q = max(0, k - C::kAcc); q < k; ++q)
-        mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
+      if (lane == 0)
+        for (int q = max(0, k - C::kAcc); q < k; ++q)
+          mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
     }
     __syncwarp();
   } else {
-    // ---------------- scaled sums: thread = token, half the tile's weight rows
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
-    constexpr int HC = BN / 2, NQ = HC / 32;
-    const int quad = warp & 3, half = (warp - 4) >> 2, c0 = half * HC;
+    // ---------------- scaled sums: thread = token, 64 weight rows
+    if (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kHigh));
+    constexpr int HC = 64;
+    const int quad = warp & 3, c0 = ((warp - 4) >> 2) * HC;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + c0;
     int k = 0;
     bool ok = true;
@@ -480,38 +502,43 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
       uint64_t acc[HC / 2];
 #pragma unroll
       for (int j = 0; j < HC / 2; ++j) acc[j] = 0ull;
-      // this half's block of weight rows (the last tile's second half may lie outside)
+      // these rows' block of weight rows (64 rows never cross one; the last tile's may lie outside)
       const int nb = min((nt * BN + c0) / kBK, (p.n_out - 1) / kBK);
       const float* swp = p.sw + (int64_t)nb * nkb;
       float sw_l = 0.f;  // lane j: weight scale of K step 32 * (kb / 32) + j
-      for (int kb = 0; kb < nkb; ++kb, ++k) {
-        if ((kb & 31) == 0) sw_l = kb + lane < nkb ? __ldg(swp + kb + lane) : 0.f;
-        const int b = k % C::kAcc;
-        ok = mbar_wait(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
-             mbar_wait(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        const float s = scale_s[(k % SL) * kBM + quad * 32 + lane] * __shfl_sync(0xffffffffu, sw_l, kb & 31);
-        const uint64_t s2 = f32x2(s, s);
-        tc_fence_after();
-        // one tcgen05.ld in flight while the one before it is summed
-        uint32_t r[2][32];
-        tmem_ld32(tl + b * BN, r[0]);
+      // The token's scales come straight from global memory, four steps ahead in registers: the
+      // MMA's operand reads keep shared memory busy, and a barrier and a read there for every
+      // step cost this loop 370 of its 1070 cycles.
+      const float* sxp = p.sx + min((int64_t)tt * kBM + quad * 32 + lane, (int64_t)p.tokens - 1);
+      float sx[4];
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          tmem_wait();
-          if (q + 1 < NQ) {
-            tmem_ld32(tl + b * BN + (q + 1) * 32, r[(q + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->accempty[b]);
+      for (int u = 0; u < 4; ++u) sx[u] = u < nkb ? __ldg(sxp + u * p.sx_ld) : 0.f;
+      for (int kb4 = 0; ok && kb4 < nkb; kb4 += 4) {
+        if ((kb4 & 31) == 0) sw_l = kb4 + lane < nkb ? __ldg(swp + kb4 + lane) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int kb = kb4 + u;
+          if (kb >= nkb) break;
+          const float s = sx[u] * __shfl_sync(0xffffffffu, sw_l, kb & 31);
+          const uint64_t s2 = f32x2(s, s);
+          sx[u] = kb + 4 < nkb ? __ldg(sxp + (int64_t)(kb + 4) * p.sx_ld) : 0.f;
+          const int b = k % C::kAcc;
+          ok = mbar_wait_spin(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
+          ++k;
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          uint32_t r[HC];
+          tmem_ld32(tl + b * C::kAccCols, r);
+          tmem_ld32(tl + b * C::kAccCols + 32, r + 32);
+          tmem_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->accempty[b]);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            acc[(q * 32 + j) / 2] = fma2((uint64_t)r[q & 1][j] | ((uint64_t)r[q & 1][j + 1] << 32), s2, acc[(q * 32 + j) / 2]);
+          for (int j = 0; j < HC; j += 2) acc[j / 2] = fma2((uint64_t)r[j] | ((uint64_t)r[j + 1] << 32), s2, acc[j / 2]);
         }
       }
       const int64_t t = (int64_t)tt * kBM + quad * 32 + lane;
@@ -571,18 +598,18 @@ struct Plan {
 };
 
 // Up to 128 tokens, or too few 128 x 128 tiles to fill the GPU: few_kernel with the narrowest
-// tile that holds the tokens (64 at most), cut over K so that about one CTA per SM streams
-// weights, each over at least 4 K steps. Else many_kernel, 256 wide unless 128 takes fewer
+// tile that holds the tokens (64 at most), cut over K while all CTAs fit on the GPU at once
+// (two per SM), each over at least 4 K steps. Else many_kernel, 192 wide unless 128 takes fewer
 // waves x width.
 Plan choose(int64_t tokens, int64_t n_out, int kblocks) {
   auto tiles = [&](int64_t w, int64_t t) { return ((n_out + w - 1) / w) * ((tokens + t - 1) / t); };
   if (tokens > 128 && tiles(128, 128) >= 100) {
-    const int64_t w256 = (tiles(256, 128) + 147) / 148 * 256, w128 = (tiles(128, 128) + 147) / 148 * 128;
-    return Plan{true, w128 < w256 ? 128 : 256, 1};
+    const int64_t w192 = (tiles(192, 128) + 147) / 148 * 192, w128 = (tiles(128, 128) + 147) / 148 * 192;
+    return Plan{true, w128 < w192 ? 128 : 192, 1};
   }
   Plan best{false, tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, 1};
   const int64_t n = tiles(kBM, best.width);
-  while (best.splits < 8 && n * best.splits * 2 <= 160 && kblocks / (best.splits * 2) >= 4) best.splits *= 2;
+  while (best.splits < 8 && n * best.splits * 2 <= 2 * 148 && kblocks / (best.splits * 2) >= 4) best.splits *= 2;
   return best;
 }
 
@@ -597,12 +624,12 @@ cudaError_t launch_many(Params& p, cudaStream_t st) {
     cudaError_t e = cudaFuncGetAttributes(&a, many_kernel<BN>);
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc would wait for ever for registers that the launch did not have
-    if (a.numRegs * kManyThreads < 128 * kLowRegs + 256 * kHighRegs) return cudaErrorInvalidConfiguration;
+    if (C::kSplitRegs && a.numRegs != C::kLaunch) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(many_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  return launch_dependent(many_kernel<BN>, dim3((unsigned)std::min(p.ntiles * p.ttiles, 148)), dim3(kManyThreads), C::kSmem, st, p);
+  return launch_dependent(many_kernel<BN>, dim3((unsigned)std::min(p.ntiles * p.ttiles, 148)), dim3(C::kThr), C::kSmem, st, p);
 }
 
 template <int BT>
@@ -617,15 +644,14 @@ cudaError_t launch_few(Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  const int nkb = (p.kblocks + p.splits - 1) / p.splits;
-  p.stages = std::min(kMaxStages, (optin - C::kFixed) / C::kStage);
-  if (p.splits == 1 && p.ntiles * p.ttiles <= 148) p.stages = std::min(p.stages, std::max(nkb, 2));
-  int smem = C::kFixed + p.stages * C::kStage;
-  // one CTA per SM: two would not fit tensor memory at the widest tiles
-  smem = std::max(smem, 116 * 1024);
+  // two CTAs share an SM's shared memory (less 1 KB each that the system keeps)
+  const int share = (228 * 1024) / C::kPerSm - 1024;
+  p.stages = std::min(C::kSlots - C::kAcc, (std::min(share, optin) - C::kFixed) / C::kStage);
+  // more than a third of the SM's shared memory: a third CTA would wait for tensor memory
+  const int smem = std::max(C::kFixed + p.stages * C::kStage, 80 * 1024);
   const int tiles = p.ntiles * p.ttiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = p.splits > 1 ? dim3((unsigned)tiles, (unsigned)p.splits) : dim3((unsigned)std::min(tiles, 148));
+  cfg.gridDim = p.splits > 1 ? dim3((unsigned)tiles, (unsigned)p.splits) : dim3((unsigned)std::min(tiles, 148 * C::kPerSm));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
@@ -648,7 +674,7 @@ cudaError_t launch_few(Params& p, cudaStream_t st) {
 using namespace harp;
 
 struct harp_layer8_s {
-  CUtensorMap tm_w, tm_w256;  // boxes of 128 and 256 rows
+  CUtensorMap tm_w, tm_w192;  // boxes of 128 and 192 rows
   int64_t n_out, n_in;
   const float* sw;
   int device;
@@ -679,7 +705,7 @@ harp_status harp_create_layer8(harp_layer8* out, int64_t n_in, int64_t n_out, co
     return encode_map_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, (uint64_t)n_in, (uint64_t)n_out, (uint64_t)row_stride,
                          l8::kBK, rows, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  if (!map(&L->tm_w, l8::kBM) || !map(&L->tm_w256, 2 * l8::kBM)) {
+  if (!map(&L->tm_w, l8::kBM) || !map(&L->tm_w192, 192)) {
     delete L;
     return set_error(HARP_ERR_CUDA, "create_layer8: cuTensorMapEncodeTiled failed");
   }
@@ -725,13 +751,13 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
   p.ys = y_stride;
   p.wide = aligned_to(y, 32) && (y_stride * dtype_bytes(yt)) % 32 == 0;
   p.wait_ns = test_hooks().wait_ns;
-  p.tm_w = nw == 256 ? L->tm_w256 : L->tm_w;
+  p.tm_w = nw == 192 ? L->tm_w192 : L->tm_w;
   if (!encode_map_2d(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)L->n_in, (uint64_t)tokens, (uint64_t)x_stride,
                      l8::kBK, (uint32_t)tw, CU_TENSOR_MAP_SWIZZLE_128B))
     return set_error(HARP_ERR_CUDA, "linear8_fwd: cuTensorMapEncodeTiled failed");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (plan.many) e = plan.width == 256 ? l8::launch_many<256>(p, st) : l8::launch_many<128>(p, st);
+  if (plan.many) e = plan.width == 192 ? l8::launch_many<192>(p, st) : l8::launch_many<128>(p, st);
   else e = plan.width == 16 ? l8::launch_few<16>(p, st) : plan.width == 32 ? l8::launch_few<32>(p, st) : l8::launch_few<64>(p, st);
   return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "linear8 launch: %s", cudaGetErrorString(e));
 }

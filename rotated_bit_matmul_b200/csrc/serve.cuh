@@ -30,6 +30,28 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block,
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// ------------------------------------------------------------------ bounded waits
+// As mbar_wait, for waits on the critical path, by one lane of a warp. Two things cost there:
+// reading %globaltimer, so the clock is only asked after many tries, and polling by whole
+// warps, so the try may sleep in the barrier until the phase completes.
+__device__ __forceinline__ bool mbar_wait_lane(uint64_t* bar, uint32_t parity, int* status, int where, uint64_t limit_ns) {
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  return mbar_wait(bar, parity, status, where, limit_ns);
+}
+// By a whole warp, polling: the shortest way from a phase's end to the code behind it.
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, int* status, int where, uint64_t limit_ns) {
+  for (int i = 0; i < 4096; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, status, where, limit_ns);
+}
+// The same for a converged warp: lane 0 waits, every lane gets the outcome.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* status, int where, uint64_t limit_ns) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_lane(bar, parity, status, where, limit_ns);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 // ------------------------------------------------------------------ vectors of eight
 // Eight consecutive values as they lie in memory: one 16-byte word (bf16, f16) or two (f32).
 struct Raw8 {
