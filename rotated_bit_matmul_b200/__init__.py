@@ -371,7 +371,7 @@ class HarpStack:
             out = torch.empty(x2.shape, dtype=out_dtype or torch.float32, device=x.device)
         ws = workspace if workspace is not None else self.cached_workspace(batch)
         with torch.cuda.device(x.device):
-            call("harp_stack_step_cached", self.handle, batch, _p(x2), _dt(x2), _p(out), _dt(out), rope.handle,
+            call("harp_stack_step_cached", self.handle, batch, _p(x2), _dt(x2), _p(out), _dt(out), rope._h,
                  cache.layer(0), cache.layer_stride, _p(positions), _p(page_table), page_table.shape[1], int(window),
                  _p(ws), ws.numel(), _stream())
         return out

@@ -1,4 +1,6 @@
-"""Compiles the CUDA sources under csrc/ into libharp.so (sm_100a) inside the package.
+"""Compiles the CUDA sources under csrc/ into libharp.so (sm_100a) inside the package, and
+csrc/torch_serving.cpp into _serving.so, the serving operators' torch-side marshalling (against
+the headers of the installed torch; skipped where torch is not installed).
 
 Usage: python -m rotated_bit_matmul_b200.build_lib [--force] [-v]
 Objects go to _build/ next to the package; the shared library is written into the
@@ -8,16 +10,20 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libharp.so")
+EXT = os.path.join(PKG, "_serving.so")
+EXT_SRC = os.path.join(CSRC, "torch_serving.cpp")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "--expt-relaxed-constexpr",
@@ -40,11 +46,38 @@ def _deps():
         [os.path.join(ROOT, "include", "harp.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def build_ext(force: bool = False) -> None:
+    torch = _torch_dir()
+    if torch is None or (not force and _newer(EXT, [EXT_SRC, os.path.join(ROOT, "include", "harp.h")])):
+        return
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DNDEBUG", *("-I" + d for d in inc), EXT_SRC, "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -61,6 +94,7 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_ext(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

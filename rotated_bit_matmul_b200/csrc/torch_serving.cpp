@@ -1,0 +1,490 @@
+// Torch-side marshalling of the serving operators: takes tensors, checks them, allocates the
+// outputs from torch's allocator and calls the C entry points of libharp.so on the tensors'
+// device and its current stream. The operators' kernels take a few microseconds at decode
+// sizes, of which a Python-side marshaller with its allocations took three times as many (one
+// residual norm of 4096 columns: 20.8 us a call).
+//
+// The C entry points are handed over by address (bind), so that this module works with the
+// library that the binding has loaded; a status other than HARP_OK goes to the binding's check,
+// which raises.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+#include <optional>
+#include <string>
+
+#include "harp.h"
+
+namespace {
+
+struct Refused {  // a ValueError
+  std::string why;
+};
+struct Raised {};  // a Python error is set
+
+decltype(&harp_rmsnorm) f_rmsnorm;
+decltype(&harp_rmsnorm_q8) f_rmsnorm_q8;
+decltype(&harp_quantize_q8) f_quantize_q8;
+decltype(&harp_quantize_weights_q8) f_quantize_weights_q8;
+decltype(&harp_linear8_fwd) f_linear8;
+decltype(&harp_rope_apply) f_rope_apply;
+decltype(&harp_rope_append) f_rope_append;
+decltype(&harp_paged_attention) f_attention;
+decltype(&harp_paged_attention_workspace_size) f_attention_ws;
+PyObject* g_check;
+
+constexpr int64_t kBlock = 128;  // columns that share one 8-bit scale
+
+void settle(harp_status st, const char* name) {
+  if (st == HARP_OK) return;
+  PyObject* r = PyObject_CallFunction(g_check, "is", (int)st, name);
+  Py_XDECREF(r);
+  throw Raised{};
+}
+
+const at::Tensor& tensor(PyObject* o, const char* what) {
+  if (!THPVariable_Check(o)) throw Refused{std::string(what) + " must be a tensor"};
+  return THPVariable_Unpack(o);
+}
+std::optional<at::Tensor> maybe(PyObject* o, const char* what) {
+  if (o == Py_None) return std::nullopt;
+  return tensor(o, what);
+}
+PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
+
+struct OneDevice {
+  int index = -2;
+  void operator()(const at::Tensor& t) {
+    if (!t.is_cuda() || (index != -2 && t.get_device() != index))
+      throw Refused{"rotated_bit_matmul_b200 works on CUDA tensors of one device only"};
+    index = (int)t.get_device();
+  }
+  void operator()(const std::optional<at::Tensor>& t) {
+    if (t) (*this)(*t);
+  }
+};
+
+harp_dtype type_of(at::ScalarType t, const char* what) {
+  switch (t) {
+    case at::kFloat: return HARP_F32;
+    case at::kBFloat16: return HARP_BF16;
+    case at::kHalf: return HARP_F16;
+    default: throw Refused{std::string(what) + " must be float32, bfloat16 or float16"};
+  }
+}
+at::ScalarType scalar_or(PyObject* o, at::ScalarType def) {
+  if (o == Py_None) return def;
+  if (!THPDtype_Check(o)) throw Refused{"a dtype is expected"};
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+at::Tensor empty(at::IntArrayRef size, at::ScalarType t, const at::Tensor& like) {
+  return at::detail::empty_cuda(size, t, like.device(), std::nullopt);
+}
+at::Tensor empty_strided(at::IntArrayRef size, at::IntArrayRef stride, at::ScalarType t, const at::Tensor& like) {
+  return at::detail::empty_strided_cuda(size, stride, t, like.device());
+}
+
+bool at16(const at::Tensor& t) { return (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0; }
+void* ptr(const std::optional<at::Tensor>& t) { return t ? t->data_ptr() : nullptr; }
+
+// rows of the last dimension, contiguous inside a row, on a 16-byte boundary
+bool rows_fit(const at::Tensor& t) {
+  return (t.size(1) <= 1 || t.stride(1) == 1) && at16(t) && (t.size(0) <= 1 || t.stride(0) >= t.size(1));
+}
+at::Tensor rows(const at::Tensor& t) {
+  at::Tensor v = t.dim() == 2 ? t : t.reshape({-1, t.size(-1)});
+  return rows_fit(v) ? v : v.clone(at::MemoryFormat::Contiguous);
+}
+int64_t row_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
+// an output the caller passed, as rows where it lies
+at::Tensor target(const at::Tensor& t, at::IntArrayRef shape, const char* what) {
+  if (t.sizes() != shape) throw Refused{std::string(what) + " has the wrong shape"};
+  at::Tensor v = t.dim() == 2 ? t : t.view({-1, t.size(-1)});
+  if (!rows_fit(v)) throw Refused{std::string(what) + " must hold its rows contiguously, on a 16-byte boundary"};
+  return v;
+}
+
+struct Norm {
+  at::Tensor x;
+  std::optional<at::Tensor> w, r, h, out_h;
+  harp_dtype xt, rt = HARP_F32, wt = HARP_F32;
+  int64_t n, r_stride = 0, h_stride = 0;
+};
+
+Norm norm_inputs(const at::Tensor& x, const std::optional<at::Tensor>& w, const std::optional<at::Tensor>& r,
+                 const std::optional<at::Tensor>& out_h) {
+  if (x.dim() < 1 || x.size(-1) < 1) throw Refused{"x needs a last dimension of at least one column"};
+  Norm a;
+  a.n = x.size(-1);
+  a.xt = type_of(x.scalar_type(), "x");
+  a.x = rows(x);
+  if (w) {
+    if (w->dim() != 1 || w->size(0) != a.n) throw Refused{"weight must have one value per column"};
+    a.wt = type_of(w->scalar_type(), "weight");
+    a.w = at16(*w) && (a.n == 1 || w->stride(0) == 1) ? *w : w->clone(at::MemoryFormat::Contiguous);
+  }
+  if (r) {
+    if (r->sizes() != x.sizes()) throw Refused{"residual must have x's shape"};
+    a.rt = type_of(r->scalar_type(), "residual");
+    a.r = rows(*r);
+    a.r_stride = row_stride(*a.r);
+    if (out_h && out_h->scalar_type() != r->scalar_type()) throw Refused{"residual_out must have the residual's dtype"};
+    a.out_h = out_h ? *out_h : empty(x.sizes(), r->scalar_type(), x);
+    a.h = target(*a.out_h, x.sizes(), "residual_out");
+    a.h_stride = row_stride(*a.h);
+  } else if (out_h) {
+    throw Refused{"residual_out without a residual"};
+  }
+  return a;
+}
+
+// e4m3 rows on 16-byte boundaries, and scales [rows, blocks] held block by block
+std::pair<at::Tensor, at::Tensor> q8_outputs(int64_t m, int64_t n, const at::Tensor& like) {
+  return {empty_strided({m, n}, {(n + 15) & ~int64_t(15), 1}, at::kFloat8_e4m3fn, like),
+          empty_strided({m, (n + kBlock - 1) / kBlock}, {1, (m + 3) & ~int64_t(3)}, at::kFloat, like)};
+}
+at::Tensor lead(const at::Tensor& t, const at::Tensor& x) {
+  if (x.dim() == 2) return t;
+  if (x.dim() == 1) return t.select(0, 0);
+  return t.unflatten(0, x.sizes().slice(0, x.dim() - 1));
+}
+
+void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
+
+PyObject* tuple2(const at::Tensor& a, const at::Tensor& b) { return Py_BuildValue("(NN)", wrap(a), wrap(b)); }
+
+// ------------------------------------------------------------------ calls
+void need(Py_ssize_t got, Py_ssize_t want) {
+  if (got != want) throw Refused{"wrong number of arguments"};
+}
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+int64_t whole(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+// x, weight, residual, eps, out_dtype, out, residual_out
+PyObject* rmsnorm(PyObject* const* a, Py_ssize_t n) {
+  need(n, 7);
+  const at::Tensor& x = tensor(a[0], "x");
+  const auto w = maybe(a[1], "weight"), r = maybe(a[2], "residual"), out = maybe(a[5], "out"), out_h = maybe(a[6], "residual_out");
+  OneDevice dev;
+  dev(x), dev(w), dev(r), dev(out), dev(out_h);
+  const Norm v = norm_inputs(x, w, r, out_h);
+  const at::Tensor y = out ? *out : empty(x.sizes(), scalar_or(a[4], x.scalar_type()), x);
+  const at::Tensor o = target(y, x.sizes(), "out");
+  const harp_dtype yt = type_of(y.scalar_type(), "out");
+  if (v.x.size(0)) {
+    const c10::cuda::CUDAGuard guard(x.device());
+    settle(f_rmsnorm(v.x.size(0), v.n, (float)real(a[3]), v.x.data_ptr(), v.xt, row_stride(v.x), ptr(v.r), v.rt, v.r_stride, ptr(v.w),
+                     v.wt, ptr(v.h), v.h_stride, o.data_ptr(), yt, row_stride(o), stream_of(dev.index)),
+           "harp_rmsnorm");
+  }
+  return r ? tuple2(y, *v.out_h) : wrap(y);
+}
+
+// x, weight, residual, eps, residual_out
+PyObject* rmsnorm_q8(PyObject* const* a, Py_ssize_t n) {
+  need(n, 5);
+  const at::Tensor& x = tensor(a[0], "x");
+  const auto w = maybe(a[1], "weight"), r = maybe(a[2], "residual"), out_h = maybe(a[4], "residual_out");
+  OneDevice dev;
+  dev(x), dev(w), dev(r), dev(out_h);
+  const Norm v = norm_inputs(x, w, r, out_h);
+  const int64_t m = v.x.size(0);
+  auto [q, s] = q8_outputs(m, v.n, x);
+  if (m) {
+    const c10::cuda::CUDAGuard guard(x.device());
+    settle(f_rmsnorm_q8(m, v.n, (float)real(a[3]), v.x.data_ptr(), v.xt, row_stride(v.x), ptr(v.r), v.rt, v.r_stride, ptr(v.w), v.wt,
+                        ptr(v.h), v.h_stride, q.data_ptr(), q.stride(0), static_cast<float*>(s.data_ptr()), s.stride(1),
+                        stream_of(dev.index)),
+           "harp_rmsnorm_q8");
+  }
+  q = lead(q, x), s = lead(s, x);
+  return r ? Py_BuildValue("(NNN)", wrap(q), wrap(s), wrap(*v.out_h)) : tuple2(q, s);
+}
+
+// x
+PyObject* quantize_q8(PyObject* const* a, Py_ssize_t n) {
+  need(n, 1);
+  const at::Tensor& x = tensor(a[0], "x");
+  OneDevice dev;
+  dev(x);
+  const Norm v = norm_inputs(x, std::nullopt, std::nullopt, std::nullopt);
+  auto [q, s] = q8_outputs(v.x.size(0), v.n, x);
+  if (v.x.size(0)) {
+    const c10::cuda::CUDAGuard guard(x.device());
+    settle(f_quantize_q8(v.x.size(0), v.n, v.x.data_ptr(), v.xt, row_stride(v.x), q.data_ptr(), q.stride(0),
+                         static_cast<float*>(s.data_ptr()), s.stride(1), stream_of(dev.index)),
+           "harp_quantize_q8");
+  }
+  return tuple2(lead(q, x), lead(s, x));
+}
+
+// W
+PyObject* quantize_weights_q8(PyObject* const* a, Py_ssize_t n) {
+  need(n, 1);
+  const at::Tensor& W = tensor(a[0], "W");
+  OneDevice dev;
+  dev(W);
+  if (W.dim() != 2 || !W.numel()) throw Refused{"W must be a matrix"};
+  const harp_dtype wt = type_of(W.scalar_type(), "W");
+  const at::Tensor w = rows(W);
+  const int64_t n_out = w.size(0), n_in = w.size(1);
+  const at::Tensor q = empty_strided({n_out, n_in}, {(n_in + 15) & ~int64_t(15), 1}, at::kFloat8_e4m3fn, W);
+  const at::Tensor s = empty({(n_out + kBlock - 1) / kBlock, (n_in + kBlock - 1) / kBlock}, at::kFloat, W);
+  const c10::cuda::CUDAGuard guard(W.device());
+  settle(f_quantize_weights_q8(n_out, n_in, w.data_ptr(), wt, row_stride(w), q.data_ptr(), q.stride(0), static_cast<float*>(s.data_ptr()),
+                               stream_of(dev.index)),
+         "harp_quantize_weights_q8");
+  return tuple2(q, s);
+}
+
+// e4m3 rows on 16-byte boundaries (a copy where they are not)
+bool wide_fit(const at::Tensor& q) {
+  return at16(q) && (q.size(1) <= 1 || q.stride(1) == 1) && (q.size(0) <= 1 || ((q.stride(0) & 15) == 0 && q.stride(0) >= q.size(1)));
+}
+at::Tensor wide(const at::Tensor& q) {
+  if (wide_fit(q)) return q;
+  at::Tensor w = empty_strided(q.sizes(), {(q.size(1) + 15) & ~int64_t(15), 1}, at::kFloat8_e4m3fn, q);
+  w.view(at::kByte).copy_(q.view(at::kByte));
+  return w;
+}
+int64_t wide_stride(const at::Tensor& q) { return q.size(0) > 1 ? q.stride(0) : (q.size(1) + 15) & ~int64_t(15); }
+
+// matrix: its wide form and that form's row stride
+PyObject* wide_rows(PyObject* const* a, Py_ssize_t n) {
+  need(n, 1);
+  const at::Tensor w = wide(tensor(a[0], "codes"));
+  return Py_BuildValue("(NL)", wrap(w), (long long)wide_stride(w));
+}
+
+// handle, codes, n_out, n_in, x, scale, out_dtype, out
+PyObject* linear8(PyObject* const* a, Py_ssize_t n) {
+  need(n, 8);
+  const at::Tensor &codes = tensor(a[1], "codes"), &x = tensor(a[4], "x"), &scale = tensor(a[5], "scale");
+  const int64_t n_out = whole(a[2]), n_in = whole(a[3]), blocks = (n_in + kBlock - 1) / kBlock;
+  const auto out = maybe(a[7], "out");
+  OneDevice dev;
+  dev(codes), dev(x), dev(scale), dev(out);
+  if (x.scalar_type() != at::kFloat8_e4m3fn || x.dim() < 1 || x.size(-1) != n_in)
+    throw Refused{"x must be float8_e4m3fn with rows of " + std::to_string(n_in)};
+  bool fits = scale.scalar_type() == at::kFloat && scale.dim() == x.dim() && scale.size(-1) == blocks;
+  for (int64_t i = 0; fits && i + 1 < x.dim(); ++i) fits = scale.size(i) == x.size(i);
+  if (!fits) throw Refused{"scale must be float32 with " + std::to_string(blocks) + " blocks for every row of x"};
+  const at::Tensor x2 = wide(x.dim() == 2 ? x : x.reshape({-1, n_in}));
+  at::Tensor s2 = x.dim() == 2 ? scale : scale.reshape({-1, blocks});
+  const int64_t m = x2.size(0);
+  int64_t ld = blocks > 1 ? s2.stride(1) : (m + 3) & ~int64_t(3);
+  if ((m > 1 && s2.stride(0) != 1) || (ld & 3) || ld < m || !at16(s2)) {
+    ld = (m + 3) & ~int64_t(3);
+    at::Tensor t = empty_strided({m, blocks}, {1, ld}, at::kFloat, x);
+    t.copy_(s2);
+    s2 = t;
+  }
+  c10::SmallVector<int64_t, 5> shape(x.sizes().begin(), x.sizes().end());
+  shape.back() = n_out;
+  const at::Tensor y = out ? *out : empty(shape, scalar_or(a[6], at::kBFloat16), x);
+  const harp_dtype yt = type_of(y.scalar_type(), "out");
+  const at::Tensor o = target(y, shape, "out");
+  if (m) {
+    const c10::cuda::CUDAGuard guard(x.device());
+    settle(f_linear8(reinterpret_cast<harp_layer8>(PyLong_AsVoidPtr(a[0])), m, x2.data_ptr(), wide_stride(x2),
+                     static_cast<const float*>(s2.data_ptr()), ld, o.data_ptr(), yt, row_stride(o), stream_of(dev.index)),
+           "harp_linear8_fwd");
+  }
+  return wrap(y);
+}
+
+at::Tensor index_of(const at::Tensor& t, int dim, const char* what) {
+  if (t.scalar_type() != at::kInt || t.dim() != dim)
+    throw Refused{std::string(what) + " must be a " + std::to_string(dim) + "-dimensional int32 tensor"};
+  return t.is_contiguous() ? t : t.contiguous();
+}
+at::Tensor heads_of(const at::Tensor& t, const char* what) {
+  if (t.dim() != 3) throw Refused{std::string(what) + " must be [tokens, heads, head_dim]"};
+  return t.stride(2) == 1 || t.size(2) == 1 ? t : t.contiguous();
+}
+
+// handle, head_dim, x, positions, inverse, out_dtype, out
+PyObject* rope_apply(PyObject* const* a, Py_ssize_t n) {
+  need(n, 7);
+  const int64_t hd = whole(a[1]);
+  const at::Tensor &x0 = tensor(a[2], "x"), &p0 = tensor(a[3], "positions");
+  const auto out = maybe(a[6], "out");
+  OneDevice dev;
+  dev(x0), dev(p0), dev(out);
+  const at::Tensor x = heads_of(x0, "x"), p = index_of(p0, 1, "positions");
+  if (x.size(0) != p.size(0) || x.size(2) != hd)
+    throw Refused{"x must be [" + std::to_string(p.size(0)) + ", heads, " + std::to_string(hd) + "]"};
+  if (out && (out->sizes() != x.sizes() || out->stride(2) != 1)) throw Refused{"out must have x's shape with a contiguous head_dim"};
+  const harp_dtype xt = type_of(x.scalar_type(), "x");
+  const at::Tensor y = out ? *out : empty(x.sizes(), scalar_or(a[5], x.scalar_type()), x);
+  const harp_dtype yt = type_of(y.scalar_type(), "out");
+  if (x.numel()) {
+    const c10::cuda::CUDAGuard guard(x.device());
+    settle(f_rope_apply(reinterpret_cast<harp_rope>(PyLong_AsVoidPtr(a[0])), x.size(0), (int)x.size(1),
+                        static_cast<const int32_t*>(p.data_ptr()), x.data_ptr(), xt, x.stride(0), x.stride(1), y.data_ptr(), yt,
+                        y.stride(0), y.stride(1), (int)whole(a[4]), stream_of(dev.index)),
+           "harp_rope_apply");
+  }
+  return wrap(y);
+}
+
+// handle, head_dim, cache address, cache k, q, k, v, positions, page_table, seq_ids, out_dtype, out
+PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
+  need(n, 12);
+  const int64_t hd = whole(a[1]);
+  const auto* cache = static_cast<const harp_kv_cache*>(PyLong_AsVoidPtr(a[2]));
+  if (!cache) throw Refused{"null cache"};
+  const at::Tensor& ck = tensor(a[3], "cache");
+  const at::Tensor &q0 = tensor(a[4], "q"), &k0 = tensor(a[5], "k"), &v0 = tensor(a[6], "v"), &p0 = tensor(a[7], "positions"),
+                   &t0 = tensor(a[8], "page_table");
+  const auto ids0 = maybe(a[9], "seq_ids"), out = maybe(a[11], "out");
+  OneDevice dev;
+  dev(ck), dev(q0), dev(k0), dev(v0), dev(p0), dev(t0), dev(ids0), dev(out);
+  const at::Tensor q = heads_of(q0, "q"), k = heads_of(k0, "k"), v = heads_of(v0, "v");
+  const at::Tensor p = index_of(p0, 1, "positions"), table = index_of(t0, 2, "page_table");
+  const int64_t tokens = p.size(0);
+  std::optional<at::Tensor> ids;
+  if (ids0) {
+    ids = index_of(*ids0, 1, "seq_ids");
+    if (ids->size(0) != tokens) throw Refused{"seq_ids must have a sequence for every token"};
+  }
+  auto is = [&](const at::Tensor& t, int64_t heads) { return t.size(0) == tokens && t.size(1) == heads && t.size(2) == hd; };
+  if (cache->head_dim != hd || !is(q, q.size(1)) || !is(k, cache->n_kv_heads) || !is(v, cache->n_kv_heads))
+    throw Refused{"q must be [" + std::to_string(tokens) + ", heads, " + std::to_string(cache->head_dim) + "], k and v the same with " +
+                  std::to_string(cache->n_kv_heads) + " heads"};
+  if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type()) throw Refused{"q, k and v must share a dtype"};
+  if (out && (out->sizes() != q.sizes() || out->stride(2) != 1)) throw Refused{"out must have q's shape with a contiguous head_dim"};
+  const harp_dtype xt = type_of(q.scalar_type(), "q");
+  const at::Tensor y = out ? *out : empty(q.sizes(), scalar_or(a[10], ck.scalar_type()), q);
+  const harp_dtype yt = type_of(y.scalar_type(), "out");
+  if (tokens) {
+    const c10::cuda::CUDAGuard guard(q.device());
+    settle(f_rope_append(reinterpret_cast<harp_rope>(PyLong_AsVoidPtr(a[0])), cache, tokens, (int)q.size(1),
+                         static_cast<const int32_t*>(p.data_ptr()), static_cast<const int32_t*>(ptr(ids)), (int)table.size(0),
+                         static_cast<const int32_t*>(table.data_ptr()), table.size(1), q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(),
+                         k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), xt, y.data_ptr(), yt, y.stride(0), y.stride(1),
+                         stream_of(dev.index)),
+           "harp_rope_append");
+  }
+  return wrap(y);
+}
+
+// cache address, cache k, q, page_table, seq_lens, scale or None, window, return_lse, out, workspace
+PyObject* paged_attention(PyObject* const* a, Py_ssize_t n) {
+  need(n, 10);
+  const auto* cache = static_cast<const harp_kv_cache*>(PyLong_AsVoidPtr(a[0]));
+  if (!cache) throw Refused{"null cache"};
+  const at::Tensor &ck = tensor(a[1], "cache"), &q0 = tensor(a[2], "q"), &t0 = tensor(a[3], "page_table"), &l0 = tensor(a[4], "seq_lens");
+  const auto out = maybe(a[8], "out"), ws0 = maybe(a[9], "workspace");
+  OneDevice dev;
+  dev(ck), dev(q0), dev(t0), dev(l0), dev(out), dev(ws0);
+  const at::Tensor table = index_of(t0, 2, "page_table"), lens = index_of(l0, 1, "seq_lens");
+  at::Tensor q = heads_of(q0, "q");
+  const int64_t m = q.size(0), heads = q.size(1), hd = q.size(2);
+  if (table.size(0) != m || lens.size(0) != m || hd != cache->head_dim)
+    throw Refused{"q, page_table, seq_lens and the cache's head_dim do not match"};
+  if (q.scalar_type() != ck.scalar_type()) throw Refused{"q must have the cache's dtype"};
+  if ((reinterpret_cast<uintptr_t>(q.data_ptr()) & 3) || (q.stride(0) & 1) || (q.stride(1) & 1)) q = q.clone(at::MemoryFormat::Contiguous);
+  if (out && (out->sizes() != q.sizes() || out->scalar_type() != q.scalar_type() || out->stride(2) != 1))
+    throw Refused{"out must have q's shape and dtype with a contiguous head_dim"};
+  const at::Tensor y = out ? *out : empty(q.sizes(), q.scalar_type(), q);
+  const bool with_lse = whole(a[7]) != 0;
+  std::optional<at::Tensor> lse;
+  if (with_lse) lse = empty({m, heads}, at::kFloat, q);
+  if (m) {
+    const c10::cuda::CUDAGuard guard(q.device());
+    size_t bytes = 0;
+    settle(f_attention_ws((int)hd, &bytes), "harp_paged_attention_workspace_size");
+    const at::Tensor ws = ws0 ? *ws0 : empty({(int64_t)bytes}, at::kByte, q);
+    if (!ws.is_contiguous()) throw Refused{"workspace must be contiguous"};
+    settle(f_attention(cache, (int)m, (int)heads, q.data_ptr(), q.stride(0), q.stride(1), static_cast<const int32_t*>(table.data_ptr()),
+                       table.size(1), static_cast<const int32_t*>(lens.data_ptr()),
+                       a[5] == Py_None ? 1.0f / std::sqrt((float)hd) : (float)real(a[5]), (int)whole(a[6]), y.data_ptr(), y.stride(0),
+                       y.stride(1), static_cast<float*>(ptr(lse)), ws.data_ptr(), ws.nbytes(), stream_of(dev.index)),
+           "harp_paged_attention");
+  }
+  return with_lse ? tuple2(y, *lse) : wrap(y);
+}
+
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    if (!g_check) throw Refused{"the entry points are not bound"};
+    PyObject* r = F(args, n);
+    if (r && PyErr_Occurred()) {  // an int argument that was none
+      Py_DECREF(r);
+      return nullptr;
+    }
+    return r;
+  } catch (const Refused& e) {
+    PyErr_SetString(PyExc_ValueError, e.why.c_str());
+  } catch (const Raised&) {
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* cls = nullptr;
+    if (PyObject* m = PyImport_ImportModule("torch")) {
+      cls = PyObject_GetAttrString(m, "OutOfMemoryError");
+      Py_DECREF(m);
+    }
+    PyErr_SetString(cls ? cls : PyExc_RuntimeError, e.what_without_backtrace());
+    Py_XDECREF(cls);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// check, then the addresses of the entry points in the order below
+PyObject* bind(PyObject*, PyObject* args) {
+  PyObject* check;
+  unsigned long long p[9];
+  if (!PyArg_ParseTuple(args, "OKKKKKKKKK", &check, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8])) return nullptr;
+  auto to = [](auto& f, unsigned long long v) { f = reinterpret_cast<std::remove_reference_t<decltype(f)>>((uintptr_t)v); };
+  to(f_rmsnorm, p[0]);
+  to(f_rmsnorm_q8, p[1]);
+  to(f_quantize_q8, p[2]);
+  to(f_quantize_weights_q8, p[3]);
+  to(f_linear8, p[4]);
+  to(f_rope_apply, p[5]);
+  to(f_rope_append, p[6]);
+  to(f_attention, p[7]);
+  to(f_attention_ws, p[8]);
+  Py_INCREF(check);
+  Py_XDECREF(g_check);
+  g_check = check;
+  Py_RETURN_NONE;
+}
+
+PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
+                         {"rmsnorm", (PyCFunction)(void (*)())guarded<rmsnorm>, METH_FASTCALL, nullptr},
+                         {"rmsnorm_q8", (PyCFunction)(void (*)())guarded<rmsnorm_q8>, METH_FASTCALL, nullptr},
+                         {"quantize_q8", (PyCFunction)(void (*)())guarded<quantize_q8>, METH_FASTCALL, nullptr},
+                         {"quantize_weights_q8", (PyCFunction)(void (*)())guarded<quantize_weights_q8>, METH_FASTCALL, nullptr},
+                         {"wide_rows", (PyCFunction)(void (*)())guarded<wide_rows>, METH_FASTCALL, nullptr},
+                         {"linear8", (PyCFunction)(void (*)())guarded<linear8>, METH_FASTCALL, nullptr},
+                         {"rope_apply", (PyCFunction)(void (*)())guarded<rope_apply>, METH_FASTCALL, nullptr},
+                         {"rope_append", (PyCFunction)(void (*)())guarded<rope_append>, METH_FASTCALL, nullptr},
+                         {"paged_attention", (PyCFunction)(void (*)())guarded<paged_attention>, METH_FASTCALL, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__serving() { return PyModule_Create(&module); }
