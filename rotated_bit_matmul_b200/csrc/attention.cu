@@ -43,8 +43,9 @@ constexpr int kRows = 16;   // query heads per tile
 constexpr int kMaxWorkers = 2 * 148 * kWarps;
 // what a pair costs beside its tiles, in tiles of 64 and of 16 keys
 constexpr int kPairCost = 2, kPairCostWarp = 3;
-constexpr int kJoinThreads = 128;
-constexpr int kJoinRows = 4;  // heads per CTA of the join
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 2;    // heads a CTA of the join takes at once
+constexpr int kJoinChunk = 256;  // partials whose weights it holds at once
 
 struct Params {
   CUtensorMap tm_k, tm_v;  // (column, row, head, page) of 2-byte elements, box {64, box_rows, 1, 1}
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
   fence_mbar_init();
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   grid_wait();
+  grid_release();  // join_kernel finds its pairs meanwhile
 
   const int per = (c.n_seqs + kThreads - 1) / kThreads;
   const int64_t total = line_total(p, red, per);
@@ -232,10 +234,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
     report(c.status, 6, 94);
     return;
   }
-  if (worker >= n) {
-    grid_release();
-    return;
-  }
+  if (worker >= n) return;
   const int64_t begin = share_begin(total, n, worker), end = share_begin(total, n, worker + 1);
 
   uint8_t* ring = smem + warp * ST * C::kStageWarp;
@@ -579,16 +578,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
         lost_phase ^= 1;
       }
     }
-  grid_release();
 }
 
 // Joins the partials of the pairs that a share border cuts. CTA (b, g): the pair cut by the
 // border in front of share b, if that is the pair's first cut; heads kJoinRows * g onward.
+// The threads of a CTA split the partials of a head as well as its columns: the partials'
+// weights are settled first, from their maxima and sums, so that the outputs are then read
+// without waiting for one another (one thread walking all 37 partials of a pair of 131072
+// positions took 25 us).
 template <int HD, int DT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+  constexpr int kCols = HD / 4, kPlaces = kJoinRows * kCols, kSplit = kJoinThreads / kPlaces;
   __shared__ int64_t red[kJoinThreads + 1 + kJoinThreads / 32];
+  __shared__ float weight[kJoinRows][kJoinChunk];
+  __shared__ float stat[kJoinRows][2];
+  __shared__ float4 part[kSplit > 1 ? kSplit - 1 : 1][kPlaces];
   const AttnCall& c = p.c;
-  grid_wait();
+  // The line depends on the lengths alone, and whatever wrote those had finished before the
+  // attention kernel, which lets this one start early, read them: only its partials are waited for.
   const int per = (c.n_seqs + kJoinThreads - 1) / kJoinThreads;
   const int64_t total = line_total(p, red, per);
   const int b = blockIdx.x + 1;
@@ -598,35 +605,79 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const Where w = locate(p, red, per, border);
   const int64_t a = w.first + p.pair_cost, e = a + w.ntiles;  // the pair's tiles on the line
   if (border <= a) return;                             // the border lies in front of the first tile
-  const int c0 = share_of(total, n, a), c1 = share_of(total, n, e - 1);
+  const int c0 = share_of(total, n, a), c1 = share_of(total, n, e - 1), parts = c1 - c0 + 1;
   if (b != c0 + 1) return;                             // not the pair's first cut
   const int kvh = w.unit / p.hblocks, hb = w.unit - kvh * p.hblocks;
   const int h0 = kvh * p.group + hb * kRows, nh = min(kRows, p.group - hb * kRows);
-  const int r0 = blockIdx.y * kJoinRows;
-  for (int i = threadIdx.x; i < kJoinRows * (HD / 4); i += kJoinThreads) {
-    const int r = r0 + i / (HD / 4), d = (i % (HD / 4)) * 4;
-    if (r >= nh) break;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = c0; x <= c1; ++x) {
-      const int64_t box = (int64_t)x * 2 + (x == c0);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (box * kRows + r) * 2);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (box * kRows + r) * HD + d);
-      const float top = fmaxf(m, ml.x);
-      const float f = m == -INFINITY ? 0.f : ex2(m - top), g = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      m = top;
-      l = l * f + ml.y * g;
-      o.x = o.x * f + v.x * g;
-      o.y = o.y * f + v.y * g;
-      o.z = o.z * f + v.z * g;
-      o.w = o.w * f + v.w * g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int place = threadIdx.x % kPlaces, slice = threadIdx.x / kPlaces;  // slice kSplit and up: idle below
+  const int pr = place / kCols, d = (place % kCols) * 4;
+  auto box = [&](int x) { return (int64_t)(c0 + x) * 2 + (x == 0); };
+  grid_wait();
+  for (int r0 = blockIdx.y * kJoinRows; r0 < nh; r0 += gridDim.y * kJoinRows) {
+    // warp i: maximum and sum of head r0 + i over all partials (a fixed tree)
+    if (warp < kJoinRows && r0 + warp < nh) {
+      float m = -INFINITY, l = 0.f;
+      for (int x = lane; x < parts; x += 32) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (box(x) * kRows + r0 + warp) * 2);
+        const float top = fmaxf(m, ml.x);
+        l = (m == -INFINITY ? 0.f : l * ex2(m - top)) + (ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top));
+        m = top;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        const float top = fmaxf(m, m2);
+        l = (m == -INFINITY ? 0.f : l * ex2(m - top)) + (m2 == -INFINITY ? 0.f : l2 * ex2(m2 - top));
+        m = top;
+      }
+      if (lane == 0) {
+        stat[warp][0] = m;
+        stat[warp][1] = l;
+      }
     }
-    const float inv = 1.f / l;
-    uint16_t* out = static_cast<uint16_t*>(c.out) + w.seq * c.o_ss + (h0 + r) * c.o_hs + d;
-    reinterpret_cast<uint32_t*>(out)[0] = pack2(o.x * inv, o.y * inv, DT);
-    reinterpret_cast<uint32_t*>(out)[1] = pack2(o.z * inv, o.w * inv, DT);
-    if (c.lse && d == 0) c.lse[(int64_t)w.seq * c.n_heads + h0 + r] = (m + log2f(l)) * 0.69314718055994530942f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < parts; x0 += kJoinChunk) {
+      const int nx = min(kJoinChunk, parts - x0);
+      __syncthreads();
+      for (int i = threadIdx.x; i < kJoinRows * nx; i += kJoinThreads) {
+        const int r = i / nx, x = i - r * nx;
+        if (r0 + r >= nh) continue;
+        const float m = p.part_ml[(box(x0 + x) * kRows + r0 + r) * 2];
+        weight[r][x] = m == -INFINITY ? 0.f : ex2(m - stat[r][0]);
+      }
+      __syncthreads();
+      if (slice < kSplit && r0 + pr < nh) {
+        const float* src = p.part_o + (r0 + pr) * HD + d;
+#pragma unroll 8
+        for (int x = slice; x < nx; x += kSplit) {
+          const float4 v = *reinterpret_cast<const float4*>(src + box(x0 + x) * (kRows * HD));
+          const float f = weight[pr][x];
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
+      }
+    }
+    if (slice > 0 && slice < kSplit) part[slice - 1][place] = o;
+    __syncthreads();
+    if (slice == 0 && r0 + pr < nh) {
+#pragma unroll
+      for (int i = 0; i + 1 < kSplit; ++i) {
+        const float4 v = part[i][place];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+      const float l = stat[pr][1], inv = 1.f / l;
+      uint16_t* out = static_cast<uint16_t*>(c.out) + w.seq * c.o_ss + (h0 + r0 + pr) * c.o_hs + d;
+      reinterpret_cast<uint32_t*>(out)[0] = pack2(o.x * inv, o.y * inv, DT);
+      reinterpret_cast<uint32_t*>(out)[1] = pack2(o.z * inv, o.w * inv, DT);
+      if (c.lse && d == 0) c.lse[(int64_t)w.seq * c.n_heads + h0 + r0 + pr] = (stat[pr][0] + log2f(l)) * 0.69314718055994530942f;
+    }
+    __syncthreads();  // stat, weight and part are free
   }
 }
 
@@ -649,7 +700,8 @@ cudaError_t launch_w(Params& p, cudaStream_t st) {
   p.part_ml = p.part_o + (int64_t)p.workers * 2 * kRows * HD;
   cudaError_t e = launch_dependent(attention_kernel<HD, DT, W>, dim3(ctas), dim3(kThreads), C::kSmem, st, p);
   if (e != cudaSuccess) return e;
-  const int groups = (min(p.group, kRows) + kJoinRows - 1) / kJoinRows;
+  // single warps leave few partials of many pairs: a CTA takes all heads of its pair
+  const int groups = W == 1 ? 1 : (std::min(p.group, kRows) + kJoinRows - 1) / kJoinRows;
   return launch_dependent(join_kernel<HD, DT>, dim3(p.workers - 1, groups), dim3(kJoinThreads), 0, st, p);
 }
 
