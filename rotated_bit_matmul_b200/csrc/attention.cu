@@ -40,7 +40,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpKeys = 16;  // keys of a tile per warp
 constexpr int kRows = 16;   // query heads per tile
-constexpr int kMaxWorkers = 2 * 148 * kWarps;
 // what a pair costs beside its tiles, in tiles of 64 and of 16 keys
 constexpr int kPairCost = 2, kPairCostWarp = 3;
 constexpr int kJoinThreads = 256;
@@ -191,8 +190,8 @@ struct Cfg {
   static constexpr int kBlocks = (HD + 63) / 64;
   static constexpr int kOperand = kBlocks * kWarpKeys * 128;      // K or V of one warp's stage
   static constexpr int kStageWarp = 2 * kOperand;
-  static constexpr int kStages = HD <= 64 ? 6 : HD <= 192 ? 3 : 2;
-  static constexpr int kCtasPerSm = HD <= 128 ? 2 : 1;
+  static constexpr int kStages = HD <= 64 ? 4 : HD <= 192 ? 3 : 2;
+  static constexpr int kCtasPerSm = HD <= 64 ? 3 : HD <= 128 ? 2 : 1;
   static constexpr int kRing = kWarps * kStages * kStageWarp;
   // W > 1: two warps' outputs and statistics; also the prefix sums of the line
   static constexpr int kScan = (kThreads + 1 + kThreads / 32) * 8;
@@ -580,104 +579,153 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
     }
 }
 
-// Joins the partials of the pairs that a share border cuts. CTA (b, g): the pair cut by the
-// border in front of share b, if that is the pair's first cut; heads kJoinRows * g onward.
-// The threads of a CTA split the partials of a head as well as its columns: the partials'
-// weights are settled first, from their maxima and sums, so that the outputs are then read
-// without waiting for one another (one thread walking all 37 partials of a pair of 131072
-// positions took 25 us).
+// Joins the partials of the pairs that a share border cuts: warp w of CTA (x, g) looks at the
+// border in front of share 8 x + w + 1 and has its pair if that is the pair's first cut. A pair
+// of up to kWarpParts partials is joined by its warp, with all loads of a value's partials in
+// flight together. One of more is joined by the whole CTA, the CTAs g taking kJoinRows heads
+// each: the partials' weights are settled first, from their maxima and sums, so that the
+// outputs are then read without waiting for one another (one thread walking all 37 partials
+// of a pair of 131072 positions took 25 us; whole CTAs for the pairs of two partials of a
+// batch of 128 short sequences, 74 us).
+constexpr int kJoinWarps = kJoinThreads / 32, kWarpParts = 8;
+
+struct Cut {
+  int parts;   // 0: no pair
+  int first;   // the first share with a part
+  int seq, h0, nh;
+};
+
 template <int HD, int DT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   constexpr int kCols = HD / 4, kPlaces = kJoinRows * kCols, kSplit = kJoinThreads / kPlaces;
   __shared__ int64_t red[kJoinThreads + 1 + kJoinThreads / 32];
+  __shared__ Cut cuts[kJoinWarps];
   __shared__ float weight[kJoinRows][kJoinChunk];
   __shared__ float stat[kJoinRows][2];
   __shared__ float4 part[kSplit > 1 ? kSplit - 1 : 1][kPlaces];
   const AttnCall& c = p.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // The line depends on the lengths alone, and whatever wrote those had finished before the
   // attention kernel, which lets this one start early, read them: only its partials are waited for.
   const int per = (c.n_seqs + kJoinThreads - 1) / kJoinThreads;
   const int64_t total = line_total(p, red, per);
-  const int b = blockIdx.x + 1;
-  const int n = shares(p, total);
-  if (b >= n) return;
-  const int64_t border = share_begin(total, n, b);
-  const Where w = locate(p, red, per, border);
-  const int64_t a = w.first + p.pair_cost, e = a + w.ntiles;  // the pair's tiles on the line
-  if (border <= a) return;                             // the border lies in front of the first tile
-  const int c0 = share_of(total, n, a), c1 = share_of(total, n, e - 1), parts = c1 - c0 + 1;
-  if (b != c0 + 1) return;                             // not the pair's first cut
-  const int kvh = w.unit / p.hblocks, hb = w.unit - kvh * p.hblocks;
-  const int h0 = kvh * p.group + hb * kRows, nh = min(kRows, p.group - hb * kRows);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = shares(p, total), b = blockIdx.x * kJoinWarps + warp + 1;
+  Cut cut{};
+  if (b < n) {
+    const int64_t border = share_begin(total, n, b);
+    const Where w = locate(p, red, per, border);
+    const int64_t a = w.first + p.pair_cost, e = a + w.ntiles;  // the pair's tiles on the line
+    cut.first = share_of(total, n, a);
+    // the border lies behind the pair's first tile, and no other border in between
+    if (border > a && b == cut.first + 1) cut.parts = share_of(total, n, e - 1) - cut.first + 1;
+    const int kvh = w.unit / p.hblocks, hb = w.unit - kvh * p.hblocks;
+    cut.seq = w.seq;
+    cut.h0 = kvh * p.group + hb * kRows;
+    cut.nh = min(kRows, p.group - hb * kRows);
+  }
+  if (lane == 0) cuts[warp] = cut;
+  grid_wait();  // every CTA, also one without a pair: the kernel after this one relies on it
+  grid_release();
+
+  auto box = [](const Cut& t, int x) { return (int64_t)(t.first + x) * 2 + (x == 0); };
+  auto put = [&](const Cut& t, int r, int d, const float4& o, float m, float l) {
+    const float inv = 1.f / l;
+    uint16_t* out = static_cast<uint16_t*>(c.out) + t.seq * c.o_ss + (t.h0 + r) * c.o_hs + d;
+    reinterpret_cast<uint32_t*>(out)[0] = pack2(o.x * inv, o.y * inv, DT);
+    reinterpret_cast<uint32_t*>(out)[1] = pack2(o.z * inv, o.w * inv, DT);
+    if (c.lse && d == 0) c.lse[(int64_t)t.seq * c.n_heads + t.h0 + r] = (m + log2f(l)) * 0.69314718055994530942f;
+  };
+  auto add = [](float4& o, float f, const float4& v) {
+    o.x = fmaf(f, v.x, o.x);
+    o.y = fmaf(f, v.y, o.y);
+    o.z = fmaf(f, v.z, o.z);
+    o.w = fmaf(f, v.w, o.w);
+  };
+  if (cut.parts > 0 && cut.parts <= kWarpParts) {
+    // heads r0, r0 + 1 with r0 = kJoinRows * (g + gridDim.y k)
+    for (int i = lane;; i += 32) {
+      const int pair = i / kPlaces, r = (blockIdx.y + pair * gridDim.y) * kJoinRows + (i % kPlaces) / kCols, d = (i % kCols) * 4;
+      if ((blockIdx.y + pair * gridDim.y) * kJoinRows >= cut.nh) break;
+      if (r >= cut.nh) continue;
+      float2 ml[kWarpParts];
+      float4 v[kWarpParts];
+#pragma unroll
+      for (int x = 0; x < kWarpParts; ++x)
+        if (x < cut.parts) {
+          const int64_t row = box(cut, x) * kRows + r;
+          ml[x] = *reinterpret_cast<const float2*>(p.part_ml + row * 2);
+          v[x] = *reinterpret_cast<const float4*>(p.part_o + row * HD + d);
+        }
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kWarpParts; ++x)
+        if (x < cut.parts) m = fmaxf(m, ml[x].x);
+#pragma unroll
+      for (int x = 0; x < kWarpParts; ++x)
+        if (x < cut.parts) {
+          const float f = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - m);
+          l = fmaf(f, ml[x].y, l);
+          add(o, f, v[x]);
+        }
+      put(cut, r, d, o, m, l);
+    }
+  }
+  __syncthreads();
   const int place = threadIdx.x % kPlaces, slice = threadIdx.x / kPlaces;  // slice kSplit and up: idle below
   const int pr = place / kCols, d = (place % kCols) * 4;
-  auto box = [&](int x) { return (int64_t)(c0 + x) * 2 + (x == 0); };
-  grid_wait();
-  for (int r0 = blockIdx.y * kJoinRows; r0 < nh; r0 += gridDim.y * kJoinRows) {
-    // warp i: maximum and sum of head r0 + i over all partials (a fixed tree)
-    if (warp < kJoinRows && r0 + warp < nh) {
-      float m = -INFINITY, l = 0.f;
-      for (int x = lane; x < parts; x += 32) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (box(x) * kRows + r0 + warp) * 2);
-        const float top = fmaxf(m, ml.x);
-        l = (m == -INFINITY ? 0.f : l * ex2(m - top)) + (ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top));
-        m = top;
-      }
+  for (int k = 0; k < kJoinWarps; ++k) {
+    const Cut t = cuts[k];
+    if (t.parts <= kWarpParts) continue;
+    for (int r0 = blockIdx.y * kJoinRows; r0 < t.nh; r0 += gridDim.y * kJoinRows) {
+      // warp i: maximum and sum of head r0 + i over all partials (a fixed tree)
+      if (warp < kJoinRows && r0 + warp < t.nh) {
+        float m = -INFINITY, l = 0.f;
+        for (int x = lane; x < t.parts; x += 32) {
+          const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (box(t, x) * kRows + r0 + warp) * 2);
+          const float top = fmaxf(m, ml.x);
+          l = (m == -INFINITY ? 0.f : l * ex2(m - top)) + (ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - top));
+          m = top;
+        }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-        const float top = fmaxf(m, m2);
-        l = (m == -INFINITY ? 0.f : l * ex2(m - top)) + (m2 == -INFINITY ? 0.f : l2 * ex2(m2 - top));
-        m = top;
-      }
-      if (lane == 0) {
-        stat[warp][0] = m;
-        stat[warp][1] = l;
-      }
-    }
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < parts; x0 += kJoinChunk) {
-      const int nx = min(kJoinChunk, parts - x0);
-      __syncthreads();
-      for (int i = threadIdx.x; i < kJoinRows * nx; i += kJoinThreads) {
-        const int r = i / nx, x = i - r * nx;
-        if (r0 + r >= nh) continue;
-        const float m = p.part_ml[(box(x0 + x) * kRows + r0 + r) * 2];
-        weight[r][x] = m == -INFINITY ? 0.f : ex2(m - stat[r][0]);
-      }
-      __syncthreads();
-      if (slice < kSplit && r0 + pr < nh) {
-        const float* src = p.part_o + (r0 + pr) * HD + d;
-#pragma unroll 8
-        for (int x = slice; x < nx; x += kSplit) {
-          const float4 v = *reinterpret_cast<const float4*>(src + box(x0 + x) * (kRows * HD));
-          const float f = weight[pr][x];
-          o.x = fmaf(f, v.x, o.x);
-          o.y = fmaf(f, v.y, o.y);
-          o.z = fmaf(f, v.z, o.z);
-          o.w = fmaf(f, v.w, o.w);
+        for (int o = 16; o > 0; o >>= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+          const float top = fmaxf(m, m2);
+          l = (m == -INFINITY ? 0.f : l * ex2(m - top)) + (m2 == -INFINITY ? 0.f : l2 * ex2(m2 - top));
+          m = top;
+        }
+        if (lane == 0) {
+          stat[warp][0] = m;
+          stat[warp][1] = l;
         }
       }
-    }
-    if (slice > 0 && slice < kSplit) part[slice - 1][place] = o;
-    __syncthreads();
-    if (slice == 0 && r0 + pr < nh) {
-#pragma unroll
-      for (int i = 0; i + 1 < kSplit; ++i) {
-        const float4 v = part[i][place];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x0 = 0; x0 < t.parts; x0 += kJoinChunk) {
+        const int nx = min(kJoinChunk, t.parts - x0);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kJoinRows * nx; i += kJoinThreads) {
+          const int r = i / nx, x = i - r * nx;
+          if (r0 + r >= t.nh) continue;
+          const float m = p.part_ml[(box(t, x0 + x) * kRows + r0 + r) * 2];
+          weight[r][x] = m == -INFINITY ? 0.f : ex2(m - stat[r][0]);
+        }
+        __syncthreads();
+        if (slice < kSplit && r0 + pr < t.nh) {
+          const float* src = p.part_o + (r0 + pr) * HD + d;
+#pragma unroll 8
+          for (int x = slice; x < nx; x += kSplit)
+            add(o, weight[pr][x], *reinterpret_cast<const float4*>(src + box(t, x0 + x) * (kRows * HD)));
+        }
       }
-      const float l = stat[pr][1], inv = 1.f / l;
-      uint16_t* out = static_cast<uint16_t*>(c.out) + w.seq * c.o_ss + (h0 + r0 + pr) * c.o_hs + d;
-      reinterpret_cast<uint32_t*>(out)[0] = pack2(o.x * inv, o.y * inv, DT);
-      reinterpret_cast<uint32_t*>(out)[1] = pack2(o.z * inv, o.w * inv, DT);
-      if (c.lse && d == 0) c.lse[(int64_t)w.seq * c.n_heads + h0 + r0 + pr] = (stat[pr][0] + log2f(l)) * 0.69314718055994530942f;
+      if (slice > 0 && slice < kSplit) part[slice - 1][place] = o;
+      __syncthreads();
+      if (slice == 0 && r0 + pr < t.nh) {
+#pragma unroll
+        for (int i = 0; i + 1 < kSplit; ++i) add(o, 1.f, part[i][place]);
+        put(t, r0 + pr, d, o, stat[pr][0], stat[pr][1]);
+      }
+      __syncthreads();  // stat, weight and part are free
     }
-    __syncthreads();  // stat, weight and part are free
   }
 }
 
@@ -694,6 +742,7 @@ cudaError_t launch_w(Params& p, cudaStream_t st) {
   }
   const int ctas = 148 * C::kCtasPerSm;
   p.workers = W == 1 ? ctas * kWarps : ctas;
+  static_assert(C::kCtasPerSm == (HD <= 64 ? 3 : HD <= 128 ? 2 : 1), "attention_ws_bytes counts on it");
   p.tile_shift = W == 1 ? 4 : 6;
   p.pair_cost = W == 1 ? kPairCostWarp : kPairCost;
   p.part_o = static_cast<float*>(p.c.ws);
@@ -702,7 +751,7 @@ cudaError_t launch_w(Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // single warps leave few partials of many pairs: a CTA takes all heads of its pair
   const int groups = W == 1 ? 1 : (std::min(p.group, kRows) + kJoinRows - 1) / kJoinRows;
-  return launch_dependent(join_kernel<HD, DT>, dim3(p.workers - 1, groups), dim3(kJoinThreads), 0, st, p);
+  return launch_dependent(join_kernel<HD, DT>, dim3((p.workers - 1 + kJoinWarps - 1) / kJoinWarps, groups), dim3(kJoinThreads), 0, st, p);
 }
 
 template <int HD, int DT>
@@ -728,7 +777,11 @@ cudaError_t launch_dt(Params& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t attention_ws_bytes(int head_dim) { return (size_t)kMaxWorkers * 2 * kRows * (head_dim + 2) * sizeof(float); }
+size_t attention_ws_bytes(int head_dim) {
+  // a warp of every CTA that the GPU holds at once may be a worker; heads over 128 wide: a CTA
+  const size_t workers = 148 * (head_dim <= 64 ? 3 * kWarps : head_dim <= 128 ? 2 * kWarps : 1);
+  return workers * 2 * kRows * (head_dim + 2) * sizeof(float);
+}
 
 const char* attention_refuses(int n_seqs, int n_heads, int n_kv, int head_dim, int dt) {
   if (n_seqs < 0 || n_seqs > 65535 || n_heads < 1 || n_heads > 65535 || n_kv < 1 || n_heads % n_kv) return "bad sizes";

@@ -201,13 +201,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tslot;
+  if (warp == 0 && lane == 0 && (int)blockIdx.x < tiles) {
+    // what does not depend on the kernel before this one: the descriptors, and a request for the
+    // first stages' weights in L2 (a hint; the copies below read what is current then)
+    tma_prefetch_desc(&p.tm_w);
+    tma_prefetch_desc(&p.tm_x);
+    int nt, tt;
+    tile_at(p, blockIdx.x, nt, tt);
+    for (int kb = kb0; kb < min(kb1, kb0 + ST); ++kb) tma_prefetch_l2_2d(&p.tm_w, kb * kBK, nt * kBM);
+  }
   grid_wait();
+  grid_release();
 
   if (warp == 0) {
     // ---------------- producer
     if (lane == 0) {
-      tma_prefetch_desc(&p.tm_w);
-      tma_prefetch_desc(&p.tm_x);
       int k = 0;  // K steps of this CTA so far, over all its tiles
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
@@ -239,29 +247,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = idesc_e4m3(kBM, BT);
-      int k = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
-        for (int kb = 0; kb < nkb; ++kb, ++k) {
-          const int slot = k % ST, b = k % C::kAcc;
-          if (k >= C::kAcc && !mbar_wait_lane(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns)) ok = false;
-          if (ok && !mbar_wait_lane(&bars->full[slot], (k / ST) & 1, p.status, 104, p.wait_ns)) ok = false;
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = smem_u32(ring + (size_t)slot * C::kStage), x = a + kBM * kBK;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_e4m3(tmem + b * BT, sw128_desc(a + 32 * kk), sw128_desc(x + 32 * kk), idesc, kk != 0);
-          mma_commit(&bars->empty[slot]);
-          mma_commit(&bars->accfull[b]);
+    // ---------------- MMA issuer: the whole warp walks the steps, so that descriptors and
+    // addresses stay warp-uniform, and one lane issues
+    const uint32_t idesc = idesc_e4m3(kBM, BT);
+    const uint64_t a0 = sw128_desc(smem_u32(ring)), x0 = sw128_desc(smem_u32(ring) + kBM * kBK);
+    const bool leader = elect_lane();
+    int k = 0, slot = 0;
+    uint32_t turn = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
+      for (int kb = 0; kb < nkb; ++kb, ++k) {
+        const int b = k % C::kAcc;
+        if (k >= C::kAcc) ok = mbar_wait_spin(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns);
+        ok = ok && mbar_wait_spin(&bars->full[slot], turn, p.status, 104, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
         }
-      // the MMAs in flight end before tensor memory is freed
+        tc_fence_after();
+        const uint64_t off = (uint64_t)(slot * (C::kStage >> 4));
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_e4m3(tmem + b * BT, a0 + off + 2 * kk, x0 + off + 2 * kk, idesc, kk != 0);
+          mma_commit(&bars->accfull[b]);
+          mma_commit(&bars->empty[slot]);
+        }
+        __syncwarp();
+        if (++slot == ST) {
+          slot = 0;
+          turn ^= 1;
+        }
+      }
+    // the MMAs in flight end before tensor memory is freed
+    if (lane == 0)
       for (int q = max(0, k - C::kAcc); q < k; ++q)
         mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
-    }
     __syncwarp();
   } else {
     // ---------------- scaled sums: thread = weight row, half the tile's tokens
@@ -282,11 +302,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
         if ((kb & 31) == 0) sw_l = kb + lane < nkb ? __ldg(p.sw + (int64_t)nt * p.kblocks + kb0 + kb + lane) : 0.f;
         const float sw = __shfl_sync(0xffffffffu, sw_l, kb & 31);
         const int b = k % C::kAcc;
-        int got = 1;
-        if (lane == 0)
-          got = mbar_wait_lane(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
-                mbar_wait_lane(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
-        if (!__shfl_sync(0xffffffffu, got, 0)) {
+        ok = mbar_wait_spin(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
+             mbar_wait_spin(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
@@ -358,13 +376,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
     // this CTA's share of the tile's (token, row) places, 32 rows at a time per warp
     for (int i = split * (kThreads / 32) + warp; i < valid * (kBM / 32); i += p.splits * (kThreads / 32)) {
       const int t = i / (kBM / 32), m = (i % (kBM / 32)) * 32 + lane, n = nt * kBM + m;
-      float v = 0.f;
-      for (int s = 0; s < p.splits; ++s) v += ld_peer(part + t * kBM + m, (uint32_t)s);
+      float part_v[8], v = 0.f;  // all reads in flight together, then summed in rank order
+#pragma unroll
+      for (int s = 0; s < 8; ++s) part_v[s] = s < p.splits ? ld_peer(part + t * kBM + m, (uint32_t)s) : 0.f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) v += part_v[s];
       if (n < p.n_out) store_act(p.y, ((int64_t)tt * BT + t) * p.ys + n, p.yt, v);
     }
     cluster_sync_all();  // no tile leaves while a peer may still read it
   }
-  grid_release();
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -420,14 +440,17 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tslot;
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tm_w);
+    tma_prefetch_desc(&p.tm_x);
+  }
   grid_wait();
+  grid_release();
 
   if (warp < 4) {
     if (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLow));
     if (warp == 0 && lane == 0) {
       // ---------------- producer
-      tma_prefetch_desc(&p.tm_w);
-      tma_prefetch_desc(&p.tm_x);
       int k = 0, slot = 0;
       uint32_t turn = 1;  // parity of the phase before the slot's next one
       bool ok = true;
@@ -588,7 +611,6 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  grid_release();
 }
 
 // ------------------------------------------------------------------ choice and launch

@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(STEPS == 1 ? 1024 : 512) norm_vec_kernel(const
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int tx = threadIdx.x, T = blockDim.x;
   grid_wait();
+  grid_release();
   if (row >= p.rows) return;  // whole warps: a row has at least one
   const int n = p.n;
   const int64_t xo = row * p.xs, ro = row * p.rs;
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   grid_wait();
+  grid_release();
   if (row >= p.rows) return;
   const int n = p.n;
   const int64_t xo = row * p.xs, ro = row * p.rs;
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(256) weights_q8_kernel(const void* w, int wt, 
                                                          uint8_t* q, int64_t qs, float* scale, int64_t kblocks) {
   __shared__ float red[8];
   grid_wait();
+  grid_release();
   const int64_t r0 = (int64_t)blockIdx.y * kBlk, c0 = (int64_t)blockIdx.x * kBlk;
   const int tr = threadIdx.x >> 4, tc = (threadIdx.x & 15) * 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float v[8][8], amax = 0.f;

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int64_t token = blockIdx.x;
   const int hd = p.t.head_dim, rot = p.t.rot_dim, half = rot / 2;
   grid_wait();
+  grid_release();
   const int pos = c.positions[token];
   if (pos < 0) return;  // uniform in the CTA
   for (int i = threadIdx.x; i < half; i += kThreads) {

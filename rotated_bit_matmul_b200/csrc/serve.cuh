@@ -11,7 +11,9 @@ namespace harp {
 // may be placed while the kernel before it drains, and every thread waits here, before its
 // first access to global memory, until that kernel has finished and its writes are visible.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel's CTAs be placed (they still stop at their grid_wait).
+// Lets the next kernel's CTAs be placed as this one's leave (they still stop at their
+// grid_wait). It takes effect once every CTA of this kernel has called it, so none of them can
+// be kept off the GPU by its successors.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>
