@@ -78,50 +78,60 @@ __device__ __forceinline__ int cost_of(const Params& p, int len) {
   return t ? t + p.pair_cost : 0;
 }
 
+// Quotients of the line are mostly small: 64-bit divisions (several hundred cycles each) only
+// where they are not.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The line, held by a warp: lane i has the sequences i * per .. i * per + per - 1.
+struct Line {
+  int64_t total, upto, own;  // all places; those of the lanes up to this one; this lane's
+  int per;
+  int64_t q;                 // shares of q + 1 places (the first r) and of q; none is empty
+  int n, r;
+};
+__device__ __forceinline__ Line measure(const Params& p) {
+  Line t;
+  const int lane = threadIdx.x & 31;
+  t.per = (p.c.n_seqs + 31) >> 5;
+  int64_t s = 0;
+#pragma unroll 4
+  for (int i = 0; i < t.per; ++i) {
+    const int seq = lane * t.per + i;
+    if (seq < p.c.n_seqs) s += cost_of(p, keys_of(p, seq));
+  }
+  t.own = s *= p.units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  t.upto = s;
+  t.total = __shfl_sync(0xffffffffu, s, 31);
+  t.n = (int)min((int64_t)p.workers, t.total);
+  t.q = t.n ? quotient(t.total, t.n) : 0;
+  t.r = (int)(t.total - t.q * t.n);
+  return t;
+}
+__device__ __forceinline__ int64_t share_begin(const Line& t, int c) { return c * t.q + min(c, t.r); }
+// the share that holds place x
+__device__ __forceinline__ int share_of(const Line& t, int64_t x) {
+  const int64_t wide = t.r * (t.q + 1);
+  return x < wide ? (int)quotient(x, t.q + 1) : t.r + (int)quotient(x - wide, t.q);
+}
+
 // A place on the line: place 0 .. pair_cost - 1 of a pair stands before its first tile.
 struct Where {
   int seq, unit, ntiles, len;
   int64_t first;  // the pair's first place
 };
-
-// Length of the line, with its prefix sums by thread in `red` (blockDim.x + 1 +
-// blockDim.x / 32 int64). All threads of the CTA.
-__device__ int64_t line_total(const Params& p, int64_t* red, int per) {
-  int64_t s = 0;
-  for (int i = 0; i < per; ++i) {
-    const int seq = threadIdx.x * per + i;
-    if (seq < p.c.n_seqs) s += cost_of(p, keys_of(p, seq));
-  }
-  s *= p.units;
-  // inclusive scan in the warp, then over the warps
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t t = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += t;
-  }
-  int64_t* wsum = red + blockDim.x + 1;
-  if (lane == 31) wsum[warp] = s;
-  __syncthreads();
-  for (int i = 0; i < warp; ++i) s += wsum[i];
-  red[threadIdx.x + 1] = s;
-  if (threadIdx.x == 0) red[0] = 0;
-  __syncthreads();
-  return red[blockDim.x];
-}
-
-__device__ Where locate(const Params& p, const int64_t* red, int per, int64_t at) {
-  // thread whose sequences hold `at`: the last prefix <= at
-  int lo = 0, hi = (int)blockDim.x;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (red[mid] <= at) lo = mid;
-    else hi = mid;
-  }
+__device__ __forceinline__ Where locate(const Params& p, const Line& t, int64_t at) {  // whole warp
+  const int src = __ffs(__ballot_sync(0xffffffffu, t.upto > at)) - 1;
+  int64_t base = __shfl_sync(0xffffffffu, t.upto - t.own, src);
   Where w;
-  int64_t base = red[lo];
   int cost;
-  w.seq = lo * per;
+  w.seq = src * t.per;
   for (;; ++w.seq) {
     w.len = keys_of(p, w.seq);
     cost = cost_of(p, w.len);
@@ -130,16 +140,10 @@ __device__ Where locate(const Params& p, const int64_t* red, int per, int64_t at
     base += n;
   }
   w.ntiles = cost - p.pair_cost;
-  w.unit = (int)((at - base) / cost);
+  w.unit = (int)quotient(at - base, cost);
   w.first = base + (int64_t)w.unit * cost;
   return w;
 }
-
-// shares of the line: none is empty
-__device__ __forceinline__ int shares(const Params& p, int64_t total) { return (int)min((int64_t)p.workers, total); }
-__device__ __forceinline__ int64_t share_begin(int64_t total, int n, int64_t c) { return c * total / n; }
-// the share that holds place x
-__device__ __forceinline__ int share_of(int64_t total, int n, int64_t x) { return (int)(((x + 1) * n - 1) / total); }
 
 // ------------------------------------------------------------------ matrix helpers
 __device__ __forceinline__ float ex2(float x) {
@@ -193,12 +197,11 @@ struct Cfg {
   static constexpr int kStages = HD <= 64 ? 4 : HD <= 192 ? 3 : 2;
   static constexpr int kCtasPerSm = HD <= 64 ? 3 : HD <= 128 ? 2 : 1;
   static constexpr int kRing = kWarps * kStages * kStageWarp;
-  // W > 1: two warps' outputs and statistics; also the prefix sums of the line
-  static constexpr int kScan = (kThreads + 1 + kThreads / 32) * 8;
-  static constexpr int kMerge = W > 1 ? 2 * kRows * HD * 4 + 2 * kRows * 2 * 4 : (kScan + 15) / 16 * 16;
+  // W > 1: half the heads of every warp's output, and the statistics
+  static constexpr int kBoxRows = kRows / 2;
+  static constexpr int kMerge = W > 1 ? kWarps * kBoxRows * (HD + 2) * 4 : 0;
   static constexpr int kQ = HD > 128 ? kBlocks * kRows * 128 : 0;  // wide heads read q from shared memory
   static constexpr int kSmem = kRing + kMerge + kQ + kWarps * kStages * 8;
-  static_assert(kMerge >= kScan, "the prefix sums lie in the merge boxes");
 };
 
 template <int HD, int DT, int W>
@@ -206,18 +209,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
   using C = Cfg<HD, W>;
   constexpr int ST = C::kStages, KS = HD / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
-  int64_t* red = reinterpret_cast<int64_t*>(smem + C::kRing);  // before the merge boxes are in use
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const AttnCall& c = p.c;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kMerge + C::kQ) + warp * ST;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
   if (lane < ST) mbar_init(&full[lane], 1);
   fence_mbar_init();
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   grid_wait();
   grid_release();  // join_kernel finds its pairs meanwhile
 
-  const int per = (c.n_seqs + kThreads - 1) / kThreads;
-  const int64_t total = line_total(p, red, per);
+  const Line line = measure(p);
   // sequences without keys: their rows are zero (split over the CTAs)
   for (int s = blockIdx.x; s < c.n_seqs; s += gridDim.x) {
     if ((int64_t)c.lens[s] + c.len_add > c.max_pages * c.page_size) report(c.status, 6 /* HARP_ERR_DEVICE_CHECK */, 93);
@@ -227,19 +232,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
     if (c.lse)
       for (int i = threadIdx.x; i < c.n_heads; i += kThreads) c.lse[(int64_t)s * c.n_heads + i] = -INFINITY;
   }
-  const int n = shares(p, total);
   const int worker = W == 1 ? blockIdx.x * kWarps + warp : blockIdx.x;
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle needs it; the launch gives it
     report(c.status, 6, 94);
     return;
   }
-  if (worker >= n) return;
-  const int64_t begin = share_begin(total, n, worker), end = share_begin(total, n, worker + 1);
+  if (worker >= line.n) return;
+  const int64_t begin = share_begin(line, worker), end = share_begin(line, worker + 1);
 
   uint8_t* ring = smem + warp * ST * C::kStageWarp;
   const uint32_t ring_s = smem_u32(ring);
-  float* merge_o = reinterpret_cast<float*>(smem + C::kRing);        // [2][kRows][HD]
-  float* merge_ml = merge_o + 2 * kRows * HD;                        // [2][kRows][2]
+  float* merge_o = reinterpret_cast<float*>(smem + C::kRing);        // [kWarps][kBoxRows][HD]
+  float* merge_ml = merge_o + kWarps * C::kBoxRows * HD;             // [kWarps][kBoxRows][2]
   uint8_t* q_sm = smem + C::kRing + C::kMerge;
 
   // A share's part of a pair: tiles [tile, stop). Places before the first tile count as 0, so a
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
     return u.stop > u.tile;
   };
   Cursor use;
-  use.w = locate(p, red, per, begin);
+  use.w = locate(p, line, begin);
   enter(use);
   bool have = use.stop > use.tile || next_pair(use);  // a share may end before its only pair's first tile
   const int box_rows = p.box_rows, boxes = kWarpKeys / box_rows;
@@ -486,73 +490,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
       l1 += __shfl_xor_sync(0xffffffffu, l1, x);
     }
 
-    // ---------------- join the four warps (1 -> 0 and 3 -> 2, then 2 -> 0), in key order
-    if (W > 1) {
-#pragma unroll
-      for (int step = 1; step <= 2; ++step) {
-        const bool gives = step == 1 ? (warp & 1) : warp == 2, takes = step == 1 ? !(warp & 1) : warp == 0;
-        const int box = step == 1 ? warp >> 1 : 0;
-        float* bo = merge_o + box * kRows * HD;
-        float* bml = merge_ml + box * kRows * 2;
-        __syncthreads();  // the boxes are free
-        if (gives) {
-#pragma unroll
-          for (int i = 0; i < HD / 8; ++i) {
-            const int d = i * 8 + (lane & 3) * 2;
-            *reinterpret_cast<float2*>(bo + row * HD + d) = make_float2(o[i][0], o[i][1]);
-            *reinterpret_cast<float2*>(bo + (row + 8) * HD + d) = make_float2(o[i][2], o[i][3]);
-          }
-          if ((lane & 3) == 0) {
-            bml[row * 2] = m0;
-            bml[row * 2 + 1] = l0;
-            bml[(row + 8) * 2] = m1;
-            bml[(row + 8) * 2 + 1] = l1;
-          }
-        }
-        __syncthreads();
-        if (takes) {
-          const float a0 = bml[row * 2], a1 = bml[(row + 8) * 2];
-          const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
-          const float g0 = a0 == -INFINITY ? 0.f : ex2(a0 - n0), g1 = a1 == -INFINITY ? 0.f : ex2(a1 - n1);
-          l0 = l0 * f0 + bml[row * 2 + 1] * g0;
-          l1 = l1 * f1 + bml[(row + 8) * 2 + 1] * g1;
-          m0 = n0;
-          m1 = n1;
-#pragma unroll
-          for (int i = 0; i < HD / 8; ++i) {
-            const int d = i * 8 + (lane & 3) * 2;
-            const float2 x = *reinterpret_cast<const float2*>(bo + row * HD + d);
-            const float2 y = *reinterpret_cast<const float2*>(bo + (row + 8) * HD + d);
-            o[i][0] = o[i][0] * f0 + x.x * g0;
-            o[i][1] = o[i][1] * f0 + x.y * g0;
-            o[i][2] = o[i][2] * f1 + y.x * g1;
-            o[i][3] = o[i][3] * f1 + y.y * g1;
-          }
-        }
-      }
-    }
-
     // ---------------- the pair's output, or this share's partial of it
-    if (W == 1 || warp == 0) {
-      if (use.tile == 0 && use.stop == use.w.ntiles) {
+    const bool whole = use.tile == 0 && use.stop == use.w.ntiles;
+    const int64_t box = (int64_t)worker * 2 + (use.tile == 0);
+    float* po = p.part_o + box * kRows * HD;
+    float* pml = p.part_ml + box * kRows * 2;
+    uint16_t* out = static_cast<uint16_t*>(c.out) + use.w.seq * c.o_ss + h0 * c.o_hs;
+    float* lse = c.lse + (int64_t)use.w.seq * c.n_heads + h0;
+    if (W == 1) {
+      if (whole) {
         const float i0 = 1.f / l0, i1 = 1.f / l1;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) {
           const int d = i * 8 + (lane & 3) * 2;
-          uint16_t* out = static_cast<uint16_t*>(c.out) + use.w.seq * c.o_ss + h0 * c.o_hs + d;
-          if (row < nh) *reinterpret_cast<uint32_t*>(out + row * c.o_hs) = pack2(o[i][0] * i0, o[i][1] * i0, DT);
-          if (row + 8 < nh) *reinterpret_cast<uint32_t*>(out + (row + 8) * c.o_hs) = pack2(o[i][2] * i1, o[i][3] * i1, DT);
+          if (row < nh) *reinterpret_cast<uint32_t*>(out + row * c.o_hs + d) = pack2(o[i][0] * i0, o[i][1] * i0, DT);
+          if (row + 8 < nh) *reinterpret_cast<uint32_t*>(out + (row + 8) * c.o_hs + d) = pack2(o[i][2] * i1, o[i][3] * i1, DT);
         }
         if (c.lse && (lane & 3) == 0) {
-          float* lse = c.lse + (int64_t)use.w.seq * c.n_heads + h0;
           if (row < nh) lse[row] = (m0 + log2f(l0)) * 0.69314718055994530942f;
           if (row + 8 < nh) lse[row + 8] = (m1 + log2f(l1)) * 0.69314718055994530942f;
         }
       } else {
-        const int64_t box = (int64_t)worker * 2 + (use.tile == 0);
-        float* po = p.part_o + box * kRows * HD;
-        float* pml = p.part_ml + box * kRows * 2;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) {
           const int d = i * 8 + (lane & 3) * 2;
@@ -560,10 +518,54 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
           if (row + 8 < nh) *reinterpret_cast<float2*>(po + (row + 8) * HD + d) = make_float2(o[i][2], o[i][3]);
         }
         if ((lane & 3) == 0) {
-          pml[row * 2] = m0;
-          pml[row * 2 + 1] = l0;
-          pml[(row + 8) * 2] = m1;
-          pml[(row + 8) * 2 + 1] = l1;
+          *reinterpret_cast<float2*>(pml + row * 2) = make_float2(m0, l0);
+          *reinterpret_cast<float2*>(pml + (row + 8) * 2) = make_float2(m1, l1);
+        }
+      }
+    } else {
+      // The four warps' parts, in the order of their keys, eight heads at a time: every warp
+      // lays its part down, and all threads add them up, four columns each.
+      for (int half = 0; half * C::kBoxRows < nh; ++half) {
+        __syncthreads();  // the boxes are free
+        if (half * C::kBoxRows + row < nh) {
+          float* bo = merge_o + (warp * C::kBoxRows + row) * HD;
+#pragma unroll
+          for (int i = 0; i < HD / 8; ++i)
+            *reinterpret_cast<float2*>(bo + i * 8 + (lane & 3) * 2) = half ? make_float2(o[i][2], o[i][3]) : make_float2(o[i][0], o[i][1]);
+          if ((lane & 3) == 0)
+            *reinterpret_cast<float2*>(merge_ml + (warp * C::kBoxRows + row) * 2) = half ? make_float2(m1, l1) : make_float2(m0, l0);
+        }
+        __syncthreads();
+        const int rows = min(C::kBoxRows, nh - half * C::kBoxRows);
+        for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
+          const int r = i / (HD / 4), d = (i % (HD / 4)) * 4, hr = half * C::kBoxRows + r;
+          float2 ml[kWarps];
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            ml[x] = *reinterpret_cast<const float2*>(merge_ml + (x * C::kBoxRows + r) * 2);
+            m = fmaxf(m, ml[x].x);
+          }
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            const float f = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - m);
+            const float4 u = *reinterpret_cast<const float4*>(merge_o + (x * C::kBoxRows + r) * HD + d);
+            l = fmaf(f, ml[x].y, l);
+            v.x = fmaf(f, u.x, v.x);
+            v.y = fmaf(f, u.y, v.y);
+            v.z = fmaf(f, u.z, v.z);
+            v.w = fmaf(f, u.w, v.w);
+          }
+          if (whole) {
+            const float inv = 1.f / l;
+            reinterpret_cast<uint32_t*>(out + hr * c.o_hs + d)[0] = pack2(v.x * inv, v.y * inv, DT);
+            reinterpret_cast<uint32_t*>(out + hr * c.o_hs + d)[1] = pack2(v.z * inv, v.w * inv, DT);
+            if (c.lse && d == 0) lse[hr] = (m + log2f(l)) * 0.69314718055994530942f;
+          } else {
+            *reinterpret_cast<float4*>(po + hr * HD + d) = v;
+            if (d == 0) *reinterpret_cast<float2*>(pml + hr * 2) = make_float2(m, l);
+          }
         }
       }
     }
@@ -598,7 +600,6 @@ struct Cut {
 template <int HD, int DT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   constexpr int kCols = HD / 4, kPlaces = kJoinRows * kCols, kSplit = kJoinThreads / kPlaces;
-  __shared__ int64_t red[kJoinThreads + 1 + kJoinThreads / 32];
   __shared__ Cut cuts[kJoinWarps];
   __shared__ float weight[kJoinRows][kJoinChunk];
   __shared__ float stat[kJoinRows][2];
@@ -607,17 +608,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // The line depends on the lengths alone, and whatever wrote those had finished before the
   // attention kernel, which lets this one start early, read them: only its partials are waited for.
-  const int per = (c.n_seqs + kJoinThreads - 1) / kJoinThreads;
-  const int64_t total = line_total(p, red, per);
-  const int n = shares(p, total), b = blockIdx.x * kJoinWarps + warp + 1;
+  const Line line = measure(p);
+  const int b = blockIdx.x * kJoinWarps + warp + 1;
   Cut cut{};
-  if (b < n) {
-    const int64_t border = share_begin(total, n, b);
-    const Where w = locate(p, red, per, border);
+  if (b < line.n) {
+    const int64_t border = share_begin(line, b);
+    const Where w = locate(p, line, border);
     const int64_t a = w.first + p.pair_cost, e = a + w.ntiles;  // the pair's tiles on the line
-    cut.first = share_of(total, n, a);
+    cut.first = share_of(line, a);
     // the border lies behind the pair's first tile, and no other border in between
-    if (border > a && b == cut.first + 1) cut.parts = share_of(total, n, e - 1) - cut.first + 1;
+    if (border > a && b == cut.first + 1) cut.parts = share_of(line, e - 1) - cut.first + 1;
     const int kvh = w.unit / p.hblocks, hb = w.unit - kvh * p.hblocks;
     cut.seq = w.seq;
     cut.h0 = kvh * p.group + hb * kRows;
