@@ -7,12 +7,13 @@
 // The angle is taken as turns, pos * f_i / 2 pi, in fp64, reduced to [-1/2, 1/2] there and
 // only then handed to sincospi in fp32: positions of any int32 size keep full precision.
 // A CTA serves one token (or a share of its heads), so every pair's cosine and sine is
-// computed once per CTA and read from shared memory by all heads of q and k. The work is
-// bound by memory: each value is read and written once with 16-byte accesses; a unit of 16
-// coordinates (both halves of 8 pairs) belongs to one thread, so q may be rotated in place.
+// computed once per CTA and shared by all heads of q and k. The work is bound by memory: each
+// value is read and written once with 16-byte accesses; a unit of 16 coordinates (both halves
+// of 8 pairs) belongs to one thread, so q may be rotated in place.
 #include "serve.cuh"
 #include "serve.h"
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -42,99 +43,208 @@ __device__ __forceinline__ int64_t cache_row(const RopeCall& c, int64_t token, i
   return (int64_t)page * c.page_stride + (int64_t)(pos % c.page_size) * c.row_stride;
 }
 
-// VEC: 16-byte accesses on units of 16 coordinates; else single pairs at any alignment
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Params p) {
-  __shared__ float cs[kMaxRotPairs], sn[kMaxRotPairs];
-  __shared__ int64_t row_s;
+// One pair of a token: coordinates e0 and e1 of one head.
+struct Unit {
+  const void* in;
+  int64_t at;   // the head's first element
+  int h, j;     // head among its kind, pair in the head
+  int kind;     // 0: q, 1: k, 2: v
+  int e0, e1;
+  bool turn;
+};
+
+__device__ __forceinline__ Unit unit_at(const Params& p, int64_t token, int u) {
   const RopeCall& c = p.c;
-  const int64_t token = blockIdx.x;
-  const int hd = p.t.head_dim, rot = p.t.rot_dim, half = rot / 2;
-  grid_wait();
-  grid_release();
-  const int pos = c.positions[token];
-  if (pos < 0) return;  // uniform in the CTA
-  for (int i = threadIdx.x; i < half; i += kThreads) {
+  constexpr int U = 2;
+  const int per_head = p.t.head_dim / U;
+  Unit x;
+  x.h = u / per_head;
+  x.j = u - x.h * per_head;
+  x.kind = x.h < c.q.heads ? 0 : x.h < c.q.heads + c.k.heads ? 1 : 2;
+  x.h -= x.kind == 0 ? 0 : x.kind == 1 ? c.q.heads : c.q.heads + c.k.heads;
+  x.turn = x.kind != 2 && x.j < p.t.rot_dim / U;
+  const bool split = x.turn && !p.t.interleaved;
+  x.e0 = split ? x.j * (U / 2) : x.j * U;
+  x.e1 = split ? x.e0 + p.t.rot_dim / 2 : x.e0 + U / 2;
+  x.in = x.kind == 0 ? c.q.in : x.kind == 1 ? c.k.in : c.v.in;
+  const int64_t ts = x.kind == 0 ? c.q.in_ts : x.kind == 1 ? c.k.in_ts : c.v.in_ts;
+  const int64_t hs = x.kind == 0 ? c.q.in_hs : x.kind == 1 ? c.k.in_hs : c.v.in_hs;
+  x.at = token * ts + x.h * hs;
+  return x;
+}
+// where it goes: base, element offset of the head and type; false: nowhere (no cache row)
+__device__ __forceinline__ bool unit_to(const Params& p, const Unit& x, int64_t token, int64_t row, void*& out, int64_t& o, int& ot) {
+  const RopeCall& c = p.c;
+  if (x.kind == 0) {
+    out = c.q.out;
+    o = token * c.q.out_ts + x.h * c.q.out_hs;
+    ot = c.yt;
+    return true;
+  }
+  out = x.kind == 1 ? c.kc : c.vc;
+  o = row + x.h * c.head_stride;
+  ot = c.ct;
+  return row >= 0;
+}
+
+// cosine and sine of the token's pairs, and the place of its cache rows, into shared memory
+template <int T>
+__device__ __forceinline__ void angles(const Params& p, int64_t token, int pos, float* cs, float* sn, int64_t* row) {
+  for (int i = threadIdx.x; i < p.t.rot_dim / 2; i += T) {
     const double turns = (double)pos * p.t.turns[i];
     float s, co;
     sincospif((float)(2.0 * (turns - rint(turns))), &s, &co);
     cs[i] = co * p.t.amplitude;
-    sn[i] = (c.inverse ? -s : s) * p.t.amplitude;
+    sn[i] = (p.c.inverse ? -s : s) * p.t.amplitude;
   }
-  if (threadIdx.x == 0) row_s = c.kc ? cache_row(c, token, pos) : 0;
+  if (threadIdx.x == T - 1) *row = p.c.kc ? cache_row(p.c, token, pos) : 0;
+}
+
+// 16-byte accesses on units of 16 coordinates. A thread keeps its unit of the head and walks
+// the heads, so that the unit's cosines and sines stay in registers; two heads are in flight at
+// a time, the first two before the angles are known. Small CTAs, twelve to an SM: 8192 tokens
+// of 32 + 32 + 32 heads of 128 bf16 take 75 us (5.4 TB/s) against 79 to 82 with 128 threads
+// (6 to 8 to an SM), and 88 with 256 threads that decode every unit anew.
+constexpr int kVecThreads = 64;
+
+struct Walk {
+  const void* in;
+  void* out;
+  int64_t in_at, in_step, out_at, out_step;  // elements: the thread's first head, and to its next
+  int n, ot;                                 // heads of this thread, output type
+};
+struct Pair2 {
+  Raw8 a[2], b[2];
+};
+
+template <int XT>
+__device__ __forceinline__ void fetch(const Walk& w, int i, int e0, int e1, Pair2& r) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (i + k < w.n) {
+      const int64_t at = w.in_at + (i + k) * w.in_step;
+      r.a[k] = raw_load8(w.in, at + e0, XT);
+      r.b[k] = raw_load8(w.in, at + e1, XT);
+    }
+}
+
+template <int XT>
+__device__ __forceinline__ void finish(const Walk& w, int i, int e0, int e1, const Pair2& r, bool turn, bool interleaved,
+                                       const float (&co)[8], const float (&si)[8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (i + k >= w.n) break;
+    float a[8], b[8];
+    raw_unpack8(r.a[k], XT, a);
+    raw_unpack8(r.b[k], XT, b);
+    if (turn) {
+      if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
+          a[2 * e] = x0 * co[e] - y0 * si[e];
+          a[2 * e + 1] = x0 * si[e] + y0 * co[e];
+          b[2 * e] = x1 * co[e + 4] - y1 * si[e + 4];
+          b[2 * e + 1] = x1 * si[e + 4] + y1 * co[e + 4];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x0 = a[e], y0 = b[e];
+          a[e] = x0 * co[e] - y0 * si[e];
+          b[e] = x0 * si[e] + y0 * co[e];
+        }
+      }
+    }
+    const int64_t at = w.out_at + (i + k) * w.out_step;
+    store8(w.out, at + e0, w.ot, a);
+    store8(w.out, at + e1, w.ot, b);
+  }
+}
+
+template <int XT>
+__global__ void __launch_bounds__(kVecThreads, 12) rope_vec_kernel(const __grid_constant__ Params p) {
+  __shared__ float cs[kMaxRotPairs], sn[kMaxRotPairs];
+  __shared__ int64_t row_s;
+  const RopeCall& c = p.c;
+  const int64_t token = blockIdx.x;
+  const int per_head = p.t.head_dim / 16, groups = kVecThreads / per_head;  // heads the CTA holds at once
+  const int j = threadIdx.x % per_head, g = blockIdx.y * groups + threadIdx.x / per_head, step = gridDim.y * groups;
+  const bool idle = (int)threadIdx.x >= groups * per_head, turn = j < p.t.rot_dim / 16, interleaved = p.t.interleaved;
+  const bool split = turn && !interleaved;
+  const int e0 = split ? j * 8 : j * 16, e1 = split ? e0 + p.t.rot_dim / 2 : e0 + 8;
+  auto count = [&](int heads) { return idle || g >= heads ? 0 : (heads - g + step - 1) / step; };
+  auto walk = [&](const HeadRows& r) {
+    return Walk{r.in, r.out, token * r.in_ts + g * r.in_hs, step * r.in_hs, token * r.out_ts + g * r.out_hs, step * r.out_hs, count(r.heads), c.yt};
+  };
+  grid_wait();
+  grid_release();
+  const int pos = c.positions[token];
+  if (pos < 0) return;  // uniform in the CTA
+  Walk w = walk(c.q);
+  Pair2 r;
+  fetch<XT>(w, 0, e0, e1, r);
+  angles<kVecThreads>(p, token, pos, cs, sn, &row_s);
   __syncthreads();
-  const int64_t row = row_s;
-  constexpr int U = VEC ? 16 : 2;   // coordinates of a unit
-  const int per_head = hd / U, rot_units = rot / U;
-  const int heads = c.q.heads + c.k.heads + c.v.heads;
-  const int units = heads * per_head;
+  float co[8], si[8];
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    // the rows of cs and sn behind rot_dim / 2 are not used (turn is false there)
+    *reinterpret_cast<float4*>(co + e) = *reinterpret_cast<const float4*>(cs + (turn ? j * 8 : 0) + e);
+    *reinterpret_cast<float4*>(si + e) = *reinterpret_cast<const float4*>(sn + (turn ? j * 8 : 0) + e);
+  }
+  for (int i = 0; i < w.n; i += 2) {
+    if (i) fetch<XT>(w, i, e0, e1, r);
+    finish<XT>(w, i, e0, e1, r, turn, interleaved, co, si);
+  }
+  if (!c.kc || row_s < 0) return;
+  w = walk(c.k);
+  w.out = c.kc;
+  w.out_at = row_s + g * c.head_stride;
+  w.out_step = step * c.head_stride;
+  w.ot = c.ct;
+  for (int i = 0; i < w.n; i += 2) {
+    fetch<XT>(w, i, e0, e1, r);
+    finish<XT>(w, i, e0, e1, r, turn, interleaved, co, si);
+  }
+  const int64_t in_at = token * c.v.in_ts + g * c.v.in_hs;
+  w.in = c.v.in;
+  w.in_at = in_at;
+  w.in_step = step * c.v.in_hs;
+  w.out = c.vc;
+  for (int i = 0; i < w.n; i += 2) {  // copied: in whole units
+    fetch<XT>(w, i, j * 16, j * 16 + 8, r);
+    finish<XT>(w, i, j * 16, j * 16 + 8, r, false, false, co, si);
+  }
+}
+
+// single pairs, at any alignment
+__global__ void __launch_bounds__(kThreads) rope_any_kernel(const __grid_constant__ Params p) {
+  __shared__ float cs[kMaxRotPairs], sn[kMaxRotPairs];
+  __shared__ int64_t row_s;
+  const RopeCall& c = p.c;
+  const int64_t token = blockIdx.x;
+  grid_wait();
+  grid_release();
+  const int pos = c.positions[token];
+  if (pos < 0) return;  // uniform in the CTA
+  angles<kThreads>(p, token, pos, cs, sn, &row_s);
+  __syncthreads();
+  const int units = (c.q.heads + c.k.heads + c.v.heads) * (p.t.head_dim / 2);
   for (int u = blockIdx.y * kThreads + threadIdx.x; u < units; u += gridDim.y * kThreads) {
-    int h = u / per_head;
-    const int j = u - h * per_head;
-    const bool is_q = h < c.q.heads, is_v = !is_q && h >= c.q.heads + c.k.heads;
-    const HeadRows& r = is_q ? c.q : is_v ? c.v : c.k;
-    if (!is_q) h -= is_v ? c.q.heads + c.k.heads : c.q.heads;
-    const bool turn = j < rot_units && !is_v;
-    // first coordinates of the unit's two runs of U / 2
-    const int e0 = !p.t.interleaved && turn ? j * (U / 2) : j * U;
-    const int e1 = !p.t.interleaved && turn ? e0 + half : e0 + U / 2;
-    const int64_t in = token * r.in_ts + h * r.in_hs;
+    const Unit x = unit_at(p, token, u);
     void* out;
     int64_t o;
     int ot;
-    if (is_q || !c.kc) {
-      out = r.out;
-      o = token * r.out_ts + h * r.out_hs;
-      ot = c.yt;
-    } else {
-      if (row < 0) continue;
-      out = is_v ? c.vc : c.kc;
-      o = row + h * c.head_stride;
-      ot = c.ct;
+    if (!unit_to(p, x, token, row_s, out, o, ot)) continue;
+    float a = load_act(x.in, x.at + x.e0, c.xt), b = load_act(x.in, x.at + x.e1, c.xt);
+    if (x.turn) {
+      const float x0 = a, y0 = b;
+      a = x0 * cs[x.j] - y0 * sn[x.j];
+      b = x0 * sn[x.j] + y0 * cs[x.j];
     }
-    const int pair = j * (U / 2);
-    if (VEC) {
-      float a[8], b[8];
-      const Raw8 ra = raw_load8(r.in, in + e0, c.xt), rb = raw_load8(r.in, in + e1, c.xt);
-      raw_unpack8(ra, c.xt, a);
-      raw_unpack8(rb, c.xt, b);
-      if (turn) {
-        float co[8], si[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *reinterpret_cast<float4*>(co + i) = *reinterpret_cast<const float4*>(cs + pair + i);
-          *reinterpret_cast<float4*>(si + i) = *reinterpret_cast<const float4*>(sn + pair + i);
-        }
-        if (p.t.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x0 = a[2 * i], y0 = a[2 * i + 1], x1 = b[2 * i], y1 = b[2 * i + 1];
-            a[2 * i] = x0 * co[i] - y0 * si[i];
-            a[2 * i + 1] = x0 * si[i] + y0 * co[i];
-            b[2 * i] = x1 * co[i + 4] - y1 * si[i + 4];
-            b[2 * i + 1] = x1 * si[i + 4] + y1 * co[i + 4];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x = a[i], y = b[i];
-            a[i] = x * co[i] - y * si[i];
-            b[i] = x * si[i] + y * co[i];
-          }
-        }
-      }
-      store8(out, o + e0, ot, a);
-      store8(out, o + e1, ot, b);
-    } else {
-      float a = load_act(r.in, in + e0, c.xt), b = load_act(r.in, in + e1, c.xt);
-      if (turn) {
-        const float x = a, y = b;
-        a = x * cs[pair] - y * sn[pair];
-        b = x * sn[pair] + y * cs[pair];
-      }
-      store_act(out, o + e0, ot, a);
-      store_act(out, o + e1, ot, b);
-    }
+    store_act(out, o + x.e0, ot, a);
+    store_act(out, o + x.e1, ot, b);
   }
 }
 
@@ -156,13 +266,15 @@ cudaError_t launch_rope(const RopeTable& t, const RopeCall& c, cudaStream_t st) 
     }
   if (c.kc) rows16(c.kc, c.page_stride, c.head_stride, c.ct), rows16(c.vc, c.row_stride, c.head_stride, c.ct);
   // a CTA serves a whole token, unless there are too few tokens to fill the GPU
-  const int64_t units = (int64_t)(c.q.heads + c.k.heads + c.v.heads) * (t.head_dim / (vec ? 16 : 2));
-  const int64_t most = (units + kThreads - 1) / kThreads;
-  int64_t share = (2 * 148 + c.tokens - 1) / c.tokens;
-  if (share > most) share = most;
+  const int64_t heads = std::max(c.q.heads, std::max(c.k.heads, c.v.heads));
+  const int64_t most = vec ? (heads + kVecThreads / (t.head_dim / 16) - 1) / (kVecThreads / (t.head_dim / 16))
+                           : ((c.q.heads + c.k.heads + c.v.heads) * (int64_t)(t.head_dim / 2) + kThreads - 1) / kThreads;
+  const int64_t share = std::min(most, (4 * 148 + c.tokens - 1) / c.tokens);
   const dim3 grid((unsigned)c.tokens, (unsigned)share);
-  if (vec) return launch_dependent(rope_kernel<true>, grid, dim3(kThreads), 0, st, p);
-  return launch_dependent(rope_kernel<false>, grid, dim3(kThreads), 0, st, p);
+  if (!vec) return launch_dependent(rope_any_kernel, grid, dim3(kThreads), 0, st, p);
+  if (c.xt == DT_F32) return launch_dependent(rope_vec_kernel<DT_F32>, grid, dim3(kVecThreads), 0, st, p);
+  if (c.xt == DT_BF16) return launch_dependent(rope_vec_kernel<DT_BF16>, grid, dim3(kVecThreads), 0, st, p);
+  return launch_dependent(rope_vec_kernel<DT_F16>, grid, dim3(kVecThreads), 0, st, p);
 }
 
 harp_status check_cache(const char* who, const harp_kv_cache* c) {
