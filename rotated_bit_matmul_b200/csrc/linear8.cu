@@ -399,7 +399,7 @@ struct Many {
   static constexpr int kAcc = BN == 192 ? 2 : 4;
   static constexpr int kAccCols = 512 / kAcc;  // tensor-memory columns from one accumulator to the next
   static constexpr int kStages = BN == 192 ? 5 : 6;
-  static constexpr int kSmem = kStages * kStage + 1024 /* barriers */ + 1024 /* alignment */;
+  static constexpr int kSmem = kStages * kStage + 1024 /* barriers */ + kSums * 2048 /* outputs */ + 1024 /* alignment */;
   // Registers: a launch of 512 threads has 128 each; the first warpgroup gives back what the
   // others take (setmaxnreg), 128 x kLow + (kThr - 128) x kHigh <= kThr x kLaunch
   static constexpr bool kSplitRegs = BN == 192;
@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int ST = C::kStages;
   Bars* bars = reinterpret_cast<Bars*>(ring + (size_t)ST * C::kStage);
+  uint32_t* out_s = reinterpret_cast<uint32_t*>(ring + (size_t)ST * C::kStage + 1024);  // 32 x 16 words per summing warp
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = p.ntiles * p.ttiles, nkb = p.kblocks;
 
@@ -564,43 +565,63 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
           for (int j = 0; j < HC; j += 2) acc[j / 2] = fma2((uint64_t)r[j] | ((uint64_t)r[j + 1] << 32), s2, acc[j / 2]);
         }
       }
-      const int64_t t = (int64_t)tt * kBM + quad * 32 + lane;
+      const int64_t t0 = (int64_t)tt * kBM + quad * 32;  // the warp's first token
       const int n0 = nt * BN + c0, valid = min(HC, p.n_out - n0);
-      if (t < p.tokens && valid > 0 && ok) {
-        auto column = [&](int j) { return __uint_as_float((uint32_t)(j & 1 ? acc[j / 2] >> 32 : acc[j / 2])); };
+      if (valid <= 0 || !ok) continue;
+      auto column = [&](int j) { return __uint_as_float((uint32_t)(j & 1 ? acc[j / 2] >> 32 : acc[j / 2])); };
+      if (p.wide && valid == HC) {  // whole 32-byte sectors from every thread
+        const int64_t t = t0 + lane;
+        if (t >= p.tokens) continue;
         if (p.yt == DT_F32) {
           float* y = static_cast<float*>(p.y) + t * p.ys + n0;
-          if (p.wide && valid == HC) {
 #pragma unroll
-            for (int j = 0; j < HC; j += 8) {
-              uint32_t v[8];
+          for (int j = 0; j < HC; j += 8) {
+            uint32_t v[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(column(j + e));
-              st_global_32(y + j, v);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < HC; ++j)
-              if (j < valid) y[j] = column(j);
+            for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(column(j + e));
+            st_global_32(y + j, v);
           }
         } else {
           uint16_t* y = static_cast<uint16_t*>(p.y) + t * p.ys + n0;
-          if (p.wide && valid == HC) {
 #pragma unroll
-            for (int j = 0; j < HC; j += 16) {
-              uint32_t v[8];
+          for (int j = 0; j < HC; j += 16) {
+            uint32_t v[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = pack2(column(j + 2 * e), column(j + 2 * e + 1), p.yt);
-              st_global_32(y + j, v);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < HC; j += 2) {
-              const uint32_t v = pack2(column(j), column(j + 1), p.yt);
-              if (j < valid) y[j] = (uint16_t)v;
-              if (j + 1 < valid) y[j + 1] = (uint16_t)(v >> 16);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = pack2(column(j + 2 * e), column(j + 2 * e + 1), p.yt);
+            st_global_32(y + j, v);
           }
+        }
+        continue;
+      }
+      // Rows at other alignments, and ragged edges: through a box of 32 tokens x 16 words, so that a
+      // warp writes runs of one token's columns (single values from 32 rows at a time took six
+      // times the product itself at 1504 x 1550 x 7399). Word w of row r lies at w ^ (r / 2 % 16).
+      uint32_t* box = out_s + (warp - 4) * 512;
+      const int rows = (int)min((int64_t)32, p.tokens - t0);
+      if (p.yt == DT_F32) {
+#pragma unroll
+        for (int j = 0; j < HC; j += 16) {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) box[lane * 16 + (e ^ ((lane >> 1) & 15))] = __float_as_uint(column(j + e));
+          __syncwarp();
+          const int col = lane & 15;
+          float* y = static_cast<float*>(p.y) + t0 * p.ys + n0 + j + col;
+          for (int r = lane >> 4; r < rows; r += 2)
+            if (j + col < valid) y[r * p.ys] = __uint_as_float(box[r * 16 + (col ^ ((r >> 1) & 15))]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < HC; j += 32) {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) box[lane * 16 + (e ^ ((lane >> 1) & 15))] = pack2(column(j + 2 * e), column(j + 2 * e + 1), p.yt);
+          __syncwarp();
+          uint16_t* y = static_cast<uint16_t*>(p.y) + t0 * p.ys + n0 + j + lane;
+          if (j + lane < valid)
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r)
+              y[r * p.ys] = (uint16_t)(box[r * 16 + ((lane >> 1) ^ ((r >> 1) & 15))] >> (16 * (lane & 1)));
         }
       }
     }
