@@ -133,7 +133,6 @@ struct Params {
   void* y;
   int yt;
   int64_t ys;
-  int wide;                // rows of y start on 32-byte boundaries
   int* status;
   uint64_t wait_ns;
 };
@@ -399,7 +398,8 @@ struct Many {
   static constexpr int kAcc = BN == 192 ? 2 : 4;
   static constexpr int kAccCols = 512 / kAcc;  // tensor-memory columns from one accumulator to the next
   static constexpr int kStages = BN == 192 ? 5 : 6;
-  static constexpr int kSmem = kStages * kStage + 1024 /* barriers */ + kSums * 2048 /* outputs */ + 1024 /* alignment */;
+  static constexpr int kSmem = kStages * kStage + 1024 /* barriers */ + 1024 /* alignment */;
+  static constexpr int kBoxes = kSums * 2048;  // outputs of the BOX form
   // Registers: a launch of 512 threads has 128 each; the first warpgroup gives back what the
   // others take (setmaxnreg), 128 x kLow + (kThr - 128) x kHigh <= kThr x kLaunch
   static constexpr bool kSplitRegs = BN == 192;
@@ -413,7 +413,9 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-template <int BN>
+// BOX: outputs at any alignment, with ragged edges; else rows of y on 32-byte boundaries and
+// whole groups of 64 weight rows. (Both in one kernel cost the second 10 % of its main loop.)
+template <int BN, bool BOX>
 __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_constant__ Params p) {
   using C = Many<BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -569,10 +571,10 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
       const int n0 = nt * BN + c0, valid = min(HC, p.n_out - n0);
       if (valid <= 0 || !ok) continue;
       auto column = [&](int j) { return __uint_as_float((uint32_t)(j & 1 ? acc[j / 2] >> 32 : acc[j / 2])); };
-      if (p.wide && valid == HC) {  // whole 32-byte sectors from every thread
+      if constexpr (!BOX) {  // whole 32-byte sectors from every thread
         const int64_t t = t0 + lane;
-        if (t >= p.tokens) continue;
-        if (p.yt == DT_F32) {
+        if (t >= p.tokens) {
+        } else if (p.yt == DT_F32) {
           float* y = static_cast<float*>(p.y) + t * p.ys + n0;
 #pragma unroll
           for (int j = 0; j < HC; j += 8) {
@@ -591,8 +593,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
             st_global_32(y + j, v);
           }
         }
-        continue;
-      }
+      } else {
       // Rows at other alignments, and ragged edges: through a box of 32 tokens x 16 words, so that a
       // warp writes runs of one token's columns (single values from 32 rows at a time took six
       // times the product itself at 1504 x 1550 x 7399). Word w of row r lies at w ^ (r / 2 % 16).
@@ -623,6 +624,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
             for (int r = 0; r < rows; ++r)
               y[r * p.ys] = (uint16_t)(box[r * 16 + ((lane >> 1) ^ ((r >> 1) & 15))] >> (16 * (lane & 1)));
         }
+      }
       }
     }
   }
@@ -656,23 +658,24 @@ Plan choose(int64_t tokens, int64_t n_out, int kblocks) {
   return best;
 }
 
-template <int BN>
+template <int BN, bool BOX>
 cudaError_t launch_many(Params& p, cudaStream_t st) {
   using C = Many<BN>;
+  constexpr int kSmem = C::kSmem + (BOX ? C::kBoxes : 0);
   int dev = 0;
   cudaGetDevice(&dev);
   static bool ready[64] = {false};  // per device
   if (dev < 0 || dev >= 64 || !ready[dev]) {
     cudaFuncAttributes a{};
-    cudaError_t e = cudaFuncGetAttributes(&a, many_kernel<BN>);
+    cudaError_t e = cudaFuncGetAttributes(&a, many_kernel<BN, BOX>);
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc would wait for ever for registers that the launch did not have
     if (C::kSplitRegs && a.numRegs != C::kLaunch) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(many_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(many_kernel<BN, BOX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  return launch_dependent(many_kernel<BN>, dim3((unsigned)std::min(p.ntiles * p.ttiles, 148)), dim3(C::kThr), C::kSmem, st, p);
+  return launch_dependent(many_kernel<BN, BOX>, dim3((unsigned)std::min(p.ntiles * p.ttiles, 148)), dim3(C::kThr), kSmem, st, p);
 }
 
 template <int BT>
@@ -792,7 +795,6 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
   p.y = y;
   p.yt = yt;
   p.ys = y_stride;
-  p.wide = aligned_to(y, 32) && (y_stride * dtype_bytes(yt)) % 32 == 0;
   p.wait_ns = test_hooks().wait_ns;
   p.tm_w = nw == 192 ? L->tm_w192 : L->tm_w;
   if (!encode_map_2d(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)L->n_in, (uint64_t)tokens, (uint64_t)x_stride,
@@ -800,7 +802,9 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
     return set_error(HARP_ERR_CUDA, "linear8_fwd: cuTensorMapEncodeTiled failed");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (plan.many) e = plan.width == 192 ? l8::launch_many<192>(p, st) : l8::launch_many<128>(p, st);
+  const bool box = !(aligned_to(y, 32) && (y_stride * dtype_bytes(yt)) % 32 == 0 && L->n_out % 64 == 0);
+  if (plan.many && plan.width == 192) e = box ? l8::launch_many<192, true>(p, st) : l8::launch_many<192, false>(p, st);
+  else if (plan.many) e = box ? l8::launch_many<128, true>(p, st) : l8::launch_many<128, false>(p, st);
   else e = plan.width == 16 ? l8::launch_few<16>(p, st) : plan.width == 32 ? l8::launch_few<32>(p, st) : l8::launch_few<64>(p, st);
   return e == cudaSuccess ? HARP_OK : set_error(HARP_ERR_CUDA, "linear8 launch: %s", cudaGetErrorString(e));
 }
