@@ -71,6 +71,22 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// A converged warp waits for two phases at once, lane 0 and lane 1 each trying one of them (a
+// try takes some 300 cycles while the tensor core reads its operands from shared memory).
+__device__ __forceinline__ bool wait_both(uint64_t* a, uint32_t pa, bool need_b, uint64_t* b, uint32_t pb, int* status,
+                                          uint64_t limit_ns) {
+  const int lane = threadIdx.x & 31;
+  uint64_t* bar = lane == 1 ? b : a;
+  const uint32_t par = lane == 1 ? pb : pa;
+  bool done = lane > 1 || (lane == 1 && !need_b);
+  for (int i = 0; i < 4096; ++i) {
+    if (!done) done = mbar_try_wait(bar, par);
+    if (__all_sync(0xffffffffu, done)) return true;
+  }
+  if (!done) done = mbar_wait(bar, par, status, lane == 1 ? 103 : 104, limit_ns);
+  return __all_sync(0xffffffffu, done);
+}
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {  // whole warp
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
                : "memory");
@@ -113,6 +129,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
+// named barriers (1 .. 15) of a CTA's warps
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -140,7 +160,7 @@ struct Params {
 template <int BT>
 struct Cfg {
   static constexpr int kStage = kBM * kBK + BT * kBK;
-  static constexpr int kAcc = BT >= 64 ? 4 : kMaxAcc;
+  static constexpr int kAcc = 4;  // <= the ring's stages
   static constexpr int kPerSm = 2;  // CTAs per SM (256 of its 512 tensor-memory columns each at most)
   // ring of token scales, one slot per K step: at least stages + accumulators (see the producer)
   static constexpr int kSlots = 16;
@@ -148,10 +168,13 @@ struct Cfg {
   static constexpr int kFixed = kSlots * BT * 4 + 1024 /* barriers */ + 1024 /* alignment */;
 };
 
-// Barrier layout (uint64 each) in the 1024 bytes behind the scale ring.
+// Barrier layout (uint64 each) in the 1024 bytes behind the scale ring. done[slot]: the MMAs of
+// the slot's K step have finished, for the producer (the stage is free) and for the summing
+// warps (the accumulator is complete). The latter cannot miss a phase: the slot's next step
+// needs an accumulator that they release after this one (accumulators <= stages).
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t accfull[kMaxAcc], accempty[kMaxAcc];
+  uint64_t full[kMaxStages], done[kMaxStages];
+  uint64_t accempty[kMaxAcc];
   uint64_t scale[kMaxSlots];
   uint32_t tslot;
 };
@@ -185,10 +208,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 1);
+      mbar_init(&bars->done[i], 1);
     }
     for (int i = 0; i < C::kAcc; ++i) {
-      mbar_init(&bars->accfull[i], 1);
       mbar_init(&bars->accempty[i], kSumWarps);
     }
     for (int i = 0; i < SL; ++i) mbar_init(&bars->scale[i], 1);
@@ -223,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
         const uint32_t sbytes = (uint32_t)(min(BT, (p.tokens - tt * BT + 3) & ~3) * 4);
         for (int kb = kb0; kb < kb1; ++kb, ++k) {
           const int slot = k % ST;
-          if (k >= ST && !mbar_wait_lane(&bars->empty[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
+          if (k >= ST && !mbar_wait_lane(&bars->done[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -257,19 +279,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
     for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
       for (int kb = 0; kb < nkb; ++kb, ++k) {
         const int b = k % C::kAcc;
-        if (k >= C::kAcc) ok = mbar_wait_spin(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns);
-        ok = ok && mbar_wait_spin(&bars->full[slot], turn, p.status, 104, p.wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = wait_both(&bars->full[slot], turn, k >= C::kAcc, &bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, p.wait_ns);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t off = (uint64_t)(slot * (C::kStage >> 4));
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_e4m3(tmem + b * BT, a0 + off + 2 * kk, x0 + off + 2 * kk, idesc, kk != 0);
-          mma_commit(&bars->accfull[b]);
-          mma_commit(&bars->empty[slot]);
+          mma_commit(&bars->done[slot]);
         }
         __syncwarp();
         if (++slot == ST) {
@@ -279,8 +296,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
       }
     // the MMAs in flight end before tensor memory is freed
     if (lane == 0)
-      for (int q = max(0, k - C::kAcc); q < k; ++q)
-        mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
+      for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->done[q % ST], (q / ST) & 1, p.status, 105, p.wait_ns);
     __syncwarp();
   } else {
     // ---------------- scaled sums: thread = weight row, half the tile's tokens
@@ -288,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
     const int quad = warp & 3, c0 = (warp >= 6 ? HC : 0);
     const int m = quad * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + c0;
-    int k = 0;
+    int k = 0, slot = 0;
+    uint32_t turn = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       int nt, tt;
@@ -302,7 +319,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
         const float sw = __shfl_sync(0xffffffffu, sw_l, kb & 31);
         const int b = k % C::kAcc;
         ok = mbar_wait_spin(&bars->scale[k % SL], (k / SL) & 1, p.status, 106, p.wait_ns) &&
-             mbar_wait_spin(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
+             mbar_wait_spin(&bars->done[slot], turn, p.status, 107, p.wait_ns);
+        if (++slot == ST) {
+          slot = 0;
+          turn ^= 1;
+        }
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -389,11 +410,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
 // ------------------------------------------------------------------ many tokens
 // Sum warps: four (the quarters of the 128 tokens) for every 64 weight rows, so that a thread
 // holds 64 sums and the 64 values of a step's block at once: one tcgen05.ld latency per step.
-// Half the warps with 128 sums each took four latencies and 1.47 ms for 4096 x 8192 x 28672.
+//
+// Hand-offs. While the tensor core reads its operands from shared memory, a try of a barrier
+// there takes some 300 cycles even when the phase is over, and with such a try by every
+// summing warp in every step, 844 cycles passed per step, of which the tensor core worked 384
+// (4096 x 8192 x 28672: 0.94 ms; pairs of CTAs with the M = 256 MMA, whose hand-offs cross the
+// pair, 1.01 ms). So a relay warp waits for the MMAs, and it and the issuer meet the summing
+// warps at named barriers, which are not in shared memory. Barrier kBarReady + b: accumulator b
+// is complete; kBarFree + b: it has been read. Neither can be passed twice by one side: the
+// next step of an accumulator needs the other side first.
+constexpr int kBarReady = 1, kBarFree = 5;
 template <int BN>
 struct Many {
   static constexpr int kSums = BN / 64 * 4;
   static constexpr int kThr = 128 + 32 * kSums;
+  static constexpr int kBarThreads = 32 * (kSums + 1);  // the summing warps and the one they meet
   static constexpr int kStage = kBM * kBK + BN * kBK;
   static constexpr int kAcc = BN == 192 ? 2 : 4;
   static constexpr int kAccCols = 512 / kAcc;  // tensor-memory columns from one accumulator to the next
@@ -429,11 +460,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 1);
-    }
-    for (int i = 0; i < C::kAcc; ++i) {
-      mbar_init(&bars->accfull[i], 1);
-      mbar_init(&bars->accempty[i], C::kSums);
+      mbar_init(&bars->done[i], 1);
     }
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -461,7 +488,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
         int nt, tt;
         tile_at(p, i, nt, tt);
         for (int kb = 0; kb < nkb; ++kb, ++k) {
-          if (k >= ST && !mbar_wait_lane(&bars->empty[slot], turn, p.status, 100, p.wait_ns)) {
+          if (k >= ST && !mbar_wait_lane(&bars->done[slot], turn, p.status, 100, p.wait_ns)) {
             ok = false;
             break;
           }
@@ -478,40 +505,50 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
       for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->full[q % ST], (q / ST) & 1, p.status, 101, p.wait_ns);
     } else if (warp == 1) {
       // ---------------- MMA issuer: the whole warp walks the steps, so that descriptors and
-      // addresses stay warp-uniform, and one lane issues
+      // addresses stay warp-uniform, and one lane issues. A step whose wait ran out is not issued;
+      // the named barriers are met all the same.
       const uint32_t idesc = idesc_e4m3(kBM, BN);
       const uint64_t a0 = sw128_desc(smem_u32(ring)), w0 = sw128_desc(smem_u32(ring) + kBM * kBK);
       const bool leader = elect_lane();
       int k = 0, slot = 0;
       uint32_t turn = 0;
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x)
+      for (int i = blockIdx.x; i < tiles; i += gridDim.x)
         for (int kb = 0; kb < nkb; ++kb, ++k) {
           const int b = k % C::kAcc;
-          if (k >= C::kAcc) ok = mbar_wait_spin(&bars->accempty[b], ((k / C::kAcc) - 1) & 1, p.status, 103, p.wait_ns);
-          ok = ok && mbar_wait_spin(&bars->full[slot], turn, p.status, 104, p.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t off = (uint64_t)(slot * (C::kStage >> 4));
-          if (leader) {
+          if (k >= C::kAcc) bar_sync(kBarFree + b, C::kBarThreads);
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(&bars->full[slot], turn, p.status, 104, p.wait_ns));
+          if (ok) {
+            tc_fence_after();
+            const uint64_t off = (uint64_t)(slot * (C::kStage >> 4));
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_e4m3(tmem + b * C::kAccCols, a0 + off + 2 * kk, w0 + off + 2 * kk, idesc, kk != 0);
-            mma_commit(&bars->accfull[b]);
-            mma_commit(&bars->empty[slot]);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_e4m3(tmem + b * C::kAccCols, a0 + off + 2 * kk, w0 + off + 2 * kk, idesc, kk != 0);
+              mma_commit(&bars->done[slot]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
           if (++slot == ST) {
             slot = 0;
             turn ^= 1;
           }
         }
-      if (lane == 0)
-        for (int q = max(0, k - C::kAcc); q < k; ++q)
-          mbar_wait(&bars->accfull[q % C::kAcc], (q / C::kAcc) & 1, p.status, 105, p.wait_ns);
+      for (int q = max(0, k - C::kAcc); q < k; ++q) bar_sync(kBarFree + q % C::kAcc, C::kBarThreads);
+    } else if (warp == 2) {
+      // ---------------- relay: waits for the MMAs of a step and lets the summing warps go
+      int k = 0, slot = 0;
+      uint32_t turn = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < tiles; i += gridDim.x)
+        for (int kb = 0; kb < nkb; ++kb, ++k) {
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(&bars->done[slot], turn, p.status, 107, p.wait_ns));
+          bar_arrive(kBarReady + k % C::kAcc, C::kBarThreads);
+          if (++slot == ST) {
+            slot = 0;
+            turn ^= 1;
+          }
+        }
     }
     __syncwarp();
   } else {
@@ -521,8 +558,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
     const int quad = warp & 3, c0 = ((warp - 4) >> 2) * HC;
     const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + c0;
     int k = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+    for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
       int nt, tt;
       tile_at(p, i, nt, tt);
       uint64_t acc[HC / 2];
@@ -539,7 +575,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
       float sx[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) sx[u] = u < nkb ? __ldg(sxp + u * p.sx_ld) : 0.f;
-      for (int kb4 = 0; ok && kb4 < nkb; kb4 += 4) {
+      for (int kb4 = 0; kb4 < nkb; kb4 += 4) {
         if ((kb4 & 31) == 0) sw_l = kb4 + lane < nkb ? __ldg(swp + kb4 + lane) : 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -549,27 +585,22 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
           const uint64_t s2 = f32x2(s, s);
           sx[u] = kb + 4 < nkb ? __ldg(sxp + (int64_t)(kb + 4) * p.sx_ld) : 0.f;
           const int b = k % C::kAcc;
-          ok = mbar_wait_spin(&bars->accfull[b], (k / C::kAcc) & 1, p.status, 107, p.wait_ns);
           ++k;
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
+          bar_sync(kBarReady + b, C::kBarThreads);
           tc_fence_after();
           uint32_t r[HC];
           tmem_ld32(tl + b * C::kAccCols, r);
           tmem_ld32(tl + b * C::kAccCols + 32, r + 32);
           tmem_wait();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->accempty[b]);
+          bar_arrive(kBarFree + b, C::kBarThreads);
 #pragma unroll
           for (int j = 0; j < HC; j += 2) acc[j / 2] = fma2((uint64_t)r[j] | ((uint64_t)r[j + 1] << 32), s2, acc[j / 2]);
         }
       }
       const int64_t t0 = (int64_t)tt * kBM + quad * 32;  // the warp's first token
       const int n0 = nt * BN + c0, valid = min(HC, p.n_out - n0);
-      if (valid <= 0 || !ok) continue;
+      if (valid <= 0) continue;
       auto column = [&](int j) { return __uint_as_float((uint32_t)(j & 1 ? acc[j / 2] >> 32 : acc[j / 2])); };
       if constexpr (!BOX) {  // whole 32-byte sectors from every thread
         const int64_t t = t0 + lane;
