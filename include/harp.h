@@ -353,8 +353,8 @@ harp_status harp_stack_step(harp_stack stack, int batch, const void* x, harp_dty
  *                  residual, or x when xt == rt, with the same stride. The norm uses h
  *                  before that rounding.
  *   y            : device [rows][n], dtype yt. May equal x when yt == xt, with the same stride.
- * h and the sums are fp32, the root is fp64. Pointers 16-byte aligned, any strides >= n; rows
- * on 16-byte boundaries take wide accesses. */
+ * All arithmetic is fp32. Pointers 16-byte aligned, any strides >= n; rows on 16-byte
+ * boundaries take wide accesses. */
 harp_status harp_rmsnorm(int64_t rows, int64_t n, float eps, const void* x, harp_dtype xt, int64_t x_stride,
                          const void* residual, harp_dtype rt, int64_t r_stride, const void* weight, harp_dtype wt,
                          void* residual_out, int64_t ro_stride, void* y, harp_dtype yt, int64_t y_stride, void* stream);

@@ -6,9 +6,9 @@
 //
 // One pass: a row's values are loaded once and stay in registers between the sum of squares
 // and the output, so the kernel moves what the formula needs and no more. The sum of squares
-// is fp32 (a thread's few values, then a fixed tree), the mean and its root are taken in
-// fp64 (once per row), and y / s is good to 1.5 units, so that a code differs from the exact
-// one only where y / s lies within fp32 rounding of the border between two codes.
+// is fp32 (a thread's few values, then a fixed tree), and y / s is good to a few units, so that
+// a code differs from the exact one only where y / s lies within fp32 rounding of the border
+// between two codes.
 //
 // Two mappings of a row onto threads:
 //   * rows that start on 16-byte boundaries: a thread holds 8 consecutive columns per step
@@ -88,9 +88,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return t;
 }
 
-__device__ __forceinline__ float inv_rms(float sum, int n, float eps) {
-  return (float)(1.0 / sqrt((double)sum / n + (double)eps));
-}
+// three roundings, and half of the first two's effect: under 2 units
+__device__ __forceinline__ float inv_rms(float sum, int n, float eps) { return 1.f / sqrtf(sum / (float)n + eps); }
 
 // blockDim = (threads per row, rows per CTA); more than one row per CTA only with 32 threads.
 // XT: type of x; RT: type of the residual, or kNone. The types are fixed at compile time so
@@ -216,9 +215,62 @@ __global__ void __launch_bounds__(STEPS == 1 ? 1024 : 512) norm_vec_kernel(const
   }
 }
 
-// the same for rows at any alignment: a warp per block of 128 columns and step
+// the same for rows at any alignment: a warp per block of 128 columns and step; whole blocks
+// take no bounds checks, and a lane's four columns lie at fixed distances from one address
+// (an address and a check per value made this 108 instructions per value, and 974 rows of 1194
+// bf16 took 10.3 us)
 // (kAny: a residual in a 16-bit type that is not x's, or in one with an fp32 x, told at run time)
 constexpr int kAny = -2;
+
+template <int T>
+struct Elem {
+  using type = uint16_t;
+};
+template <>
+struct Elem<DT_F32> {
+  using type = float;
+};
+template <int T>
+__device__ __forceinline__ float value_of(const typename Elem<T>::type* p) {
+  if constexpr (T == DT_F32) return *p;
+  else return unpack2((uint32_t)*p, T).x;
+}
+template <int T>
+__device__ __forceinline__ void put_value(typename Elem<T>::type* p, float v) {
+  if constexpr (T == DT_F32) *p = v;
+  else *p = (uint16_t)pack2(v, 0.f, T);
+}
+// four columns of a block: add them to v (or set it)
+template <int T, bool ADD>
+__device__ __forceinline__ void take4(const void* base, int64_t at, int left, float (&v)[4]) {
+  const auto* p = static_cast<const typename Elem<T>::type*>(base) + at;
+  if (left >= kBlk) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (ADD ? v[i] : 0.f) + value_of<T>(p + 32 * i);
+  } else {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = lane + 32 * i < left ? value_of<T>(p + 32 * i) : 0.f;
+      v[i] = (ADD ? v[i] : 0.f) + x;
+    }
+  }
+}
+template <int T>
+__device__ __forceinline__ void weigh4(const void* base, int64_t at, int left, float (&v)[4]) {
+  float w[4];
+  take4<T, false>(base, at, left, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] *= w[i];  // 0 behind the row, where v is 0 too
+}
+template <int T>
+__device__ __forceinline__ void put4(void* base, int64_t at, int left, const float (&v)[4]) {
+  auto* p = static_cast<typename Elem<T>::type*>(base) + at;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (left >= kBlk || lane + 32 * i < left) put_value<T>(p + 32 * i, v[i]);
+}
 
 template <int XT, int RT, int STEPS, bool Q8>
 __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ NormParams p) {
@@ -229,33 +281,31 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
   grid_release();
   if (row >= p.rows) return;
   const int n = p.n;
-  const int64_t xo = row * p.xs, ro = row * p.rs;
+  const int64_t xo = row * p.xs + lane, ro = row * p.rs + lane;
   float v[STEPS][4];
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = (k * W + warp) * kBlk + i * 32 + lane;
-      v[k][i] = c < n ? load_act(p.x, xo + c, XT) : 0.f;
-    }
+  for (int k = 0; k < STEPS; ++k) {
+    const int c0 = (k * W + warp) * kBlk;
+    take4<XT, false>(p.x, xo + c0, n - c0, v[k]);
+  }
   if (RT != kNone) {
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k)
+    for (int k = 0; k < STEPS; ++k) {
+      const int c0 = (k * W + warp) * kBlk;
+      if (RT != kAny) take4<RT == kAny || RT == kNone ? DT_F32 : RT, true>(p.r, ro + c0, n - c0, v[k]);
+      else if (p.rt == DT_BF16) take4<DT_BF16, true>(p.r, ro + c0, n - c0, v[k]);
+      else take4<DT_F16, true>(p.r, ro + c0, n - c0, v[k]);
+    }
+    if (p.h) {
+      const int64_t ho = row * p.hs + lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (k * W + warp) * kBlk + i * 32 + lane;
-        if (c < n) v[k][i] += load_act(p.r, ro + c, RT == kAny ? p.rt : RT);
+      for (int k = 0; k < STEPS; ++k) {
+        const int c0 = (k * W + warp) * kBlk;
+        if (RT != kAny) put4<RT == kAny || RT == kNone ? DT_F32 : RT>(p.h, ho + c0, n - c0, v[k]);
+        else if (p.rt == DT_BF16) put4<DT_BF16>(p.h, ho + c0, n - c0, v[k]);
+        else put4<DT_F16>(p.h, ho + c0, n - c0, v[k]);
       }
-  }
-  if (RT != kNone && p.h) {
-    const int64_t ho = row * p.hs;
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (k * W + warp) * kBlk + i * 32 + lane;
-        if (c < n) store_act(p.h, ho + c, RT == kAny ? p.rt : RT, v[k][i]);
-      }
+    }
   }
   if (p.norm) {
     float s = 0.f;
@@ -264,42 +314,44 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fmaf(v[k][i], v[k][i], s);
     const float inv = inv_rms(row_sum(s, red), n, p.eps);
-    auto weigh = [&](int wt) {
 #pragma unroll
-      for (int k = 0; k < STEPS; ++k)
+    for (int k = 0; k < STEPS; ++k) {
+      const int c0 = (k * W + warp) * kBlk;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = (k * W + warp) * kBlk + i * 32 + lane;
-          v[k][i] *= inv;
-          if (p.w && c < n) v[k][i] *= load_act(p.w, c, wt);
-        }
-    };
-    if (p.wt == XT) weigh(XT);
-    else weigh(p.wt);
+      for (int i = 0; i < 4; ++i) v[k][i] *= inv;
+      if (p.w) {
+        if (p.wt == DT_F32) weigh4<DT_F32>(p.w, c0 + lane, n - c0, v[k]);
+        else if (p.wt == DT_BF16) weigh4<DT_BF16>(p.w, c0 + lane, n - c0, v[k]);
+        else weigh4<DT_F16>(p.w, c0 + lane, n - c0, v[k]);
+      }
+    }
   }
-  const int64_t yo = row * p.ys;
+  const int64_t yo = row * p.ys + lane;
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
-    const int c0 = (k * W + warp) * kBlk;
-    if (c0 >= n) break;  // uniform in the warp
-    float s = 1.f;
+    const int c0 = (k * W + warp) * kBlk, left = n - c0;
+    if (left <= 0) break;  // uniform in the warp
     if (Q8) {
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) amax = max_nan(amax, fabsf(v[k][i]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      s = block_scale(amax);
+      const float s = block_scale(amax);
       if (lane == 0) p.scale[(int64_t)(c0 / kBlk) * p.scale_ld + row] = s;
-    }
-    float d[4];
-    if (Q8) over_scale(v[k], s, d);
+      float d[4];
+      over_scale(v[k], s, d);
+      uint8_t* q = static_cast<uint8_t*>(p.y) + yo + c0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + i * 32 + lane;
-      if (c >= n) continue;
-      if (Q8) static_cast<uint8_t*>(p.y)[yo + c] = __nv_cvt_float_to_fp8(d[i], __NV_SATFINITE, __NV_E4M3);
-      else store_act(p.y, yo + c, p.yt, v[k][i]);
+      for (int i = 0; i < 4; i += 2) {
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(d[i], d[i + 1]), __NV_SATFINITE, __NV_E4M3);
+        if (left >= kBlk || lane + 32 * i < left) q[32 * i] = (uint8_t)two;
+        if (left >= kBlk || lane + 32 * (i + 1) < left) q[32 * (i + 1)] = (uint8_t)(two >> 8);
+      }
+    } else {
+      if (p.yt == DT_F32) put4<DT_F32>(p.y, yo + c0, left, v[k]);
+      else if (p.yt == DT_BF16) put4<DT_BF16>(p.y, yo + c0, left, v[k]);
+      else put4<DT_F16>(p.y, yo + c0, left, v[k]);
     }
   }
 }
@@ -356,13 +408,13 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
                    on16(p.h, p.hs, dtype_bytes(p.rt)) && on16(p.y, p.ys, Q8 ? 1 : dtype_bytes(p.yt));
   const int per = vec ? 256 : kBlk;             // columns a warp covers per step
   const int warps = (p.n + per - 1) / per;      // with one step per thread
-  // Few rows: as many threads as the row has work for, for latency. Many: up to 4 steps per
-  // thread, so that an SM holds several rows and one row's sum hides behind another's loads
-  // (8192 x 8192 bf16 with a residual: one step 179 us).
+  // Few rows: as many threads as the row has work for, for latency. Many: four steps per thread
+  // where the row has them, one warp per row up to 1024 columns, so that an SM holds
+  // many rows and one row's sum hides behind another's loads (8192 x 8192 bf16 with a residual:
+  // one step 179 us, four 84).
   int steps = 1;
-  const int most = 4;
   if (p.rows > 2 * 148)
-    while (steps < most && warps > 4 * steps) steps *= 2;
+    while (steps < (!vec && warps <= 8 ? 8 : 4) && warps > steps) steps *= 2;
   while ((warps + steps - 1) / steps > (steps == 1 || !vec ? 32 : 16)) steps *= 2;
   const int tpr = 32 * ((warps + steps - 1) / steps);
   const int rpb = tpr == 32 ? 4 : 1;
