@@ -339,7 +339,8 @@ harp_status harp_stack_step(harp_stack stack, int batch, const void* x, harp_dty
  * paged key-value cache and the attention that reads it, and the linears that a low-bit
  * recipe leaves at 8 bits (output head, sensitive layers). Their rows may be strided views:
  * strides count elements, the innermost dimension is contiguous. Unlike the entry points
- * above, a pointer only needs the alignment its description gives. They are launched with
+ * above, a pointer only needs the alignment its description gives. Forward calls: the binding
+ * records no autograd graph (harp_rope_apply's inverse is its gradient). They are launched with
  * programmatic stream serialisation; every kernel waits for the one before it, so the order
  * of a stream holds as always. Each call can be captured into a CUDA graph after a first
  * call on the device. */
@@ -393,7 +394,8 @@ harp_status harp_create_layer8(harp_layer8* out, int64_t n_in, int64_t n_out, co
                                const float* scale, void* stream);
 harp_status harp_destroy_layer8(harp_layer8 layer);
 
-/* y for `tokens` rows (0..2^24), on the device the layer was created on.
+/* y for `tokens` rows (0..2^24; more than 2^30 tiles of 128 x 128 x 64 are refused as
+ * HARP_ERR_UNSUPPORTED), on the device the layer was created on.
  *   x       : device e4m3 [tokens][n_in], 16-byte aligned, x_stride a multiple of 16.
  *   x_scale : device fp32 [ceil(n_in / 128)][scale_ld], 16-byte aligned, scale_ld a multiple
  *             of 4, at least tokens.
@@ -441,7 +443,7 @@ harp_status harp_rope_apply(harp_rope rope, int64_t tokens, int heads, const int
  * lies in page page_table[s * max_pages + j / page_size], row j % page_size.
  * dtype bf16 or f16; page_size a power of two, at most 4096; head_dim even, at most 256; strides
  * positive multiples of 8; k and v 16-byte aligned. Page indices outside [0, n_pages) are never
- * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93) and takes their rows as 0. */
+ * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93; 95, 96: HARP_ERR_TIMEOUT of a copy) and takes their rows as 0. */
 typedef struct {
   void* k;
   void* v;

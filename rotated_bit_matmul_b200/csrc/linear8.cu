@@ -819,6 +819,9 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
   const int nw = plan.many ? plan.width : l8::kBM, tw = plan.many ? l8::kBM : plan.width;  // weight rows, tokens of a tile
   p.ntiles = (int)((L->n_out + nw - 1) / nw);
   p.ttiles = (int)((tokens + tw - 1) / tw);
+  if ((int64_t)p.ntiles * p.ttiles * p.kblocks > (int64_t(1) << 30))  // steps are counted in 32 bits
+    return set_error(HARP_ERR_UNSUPPORTED, "linear8_fwd: %lld x %lld x %lld is too large for one call", (long long)tokens,
+                     (long long)L->n_in, (long long)L->n_out);
   p.splits = plan.splits;
   p.sx = x_scale;
   p.sx_ld = scale_ld;

@@ -640,6 +640,80 @@ def test_graph_replay_follows_lengths_and_streams(rb):
     clean(rb)
 
 
+def test_back_to_back_calls_wait_for_each_other(rb):
+    """Chains whose every call reads what the one before wrote, with kernels that start before
+    their predecessors have ended: without a wait between the calls the results are those of the
+    same chain with one."""
+    g = gen(31)
+    hd, heads, kv, page, seqs = 128, 8, 2, 16, 3
+    width = heads * hd
+    table = torch.arange(seqs * 8, dtype=torch.int32, device="cuda").view(seqs, 8)
+    rope = rb.HarpRope(hd)
+    layers = [rb.HarpLinear8(*rb.harp_quantize_weights_q8(randn(g, width, width) / 20)) for _ in range(2)]
+    weight = 1 + 0.1 * randn(g, width, dtype=torch.bfloat16)
+    start = randn(g, seqs, width, dtype=torch.bfloat16)
+    kv_in = randn(g, seqs, 2 * kv, hd, dtype=torch.bfloat16)
+
+    def chain(wait):
+        cache = rb.HarpCache.empty(1, seqs * 8, kv, page, hd)
+        x, res = start, torch.zeros_like(start)
+        lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+        out = []
+        for t in range(60):
+            pos = lens.clone()
+            lens += 1
+            q, s, res = rb.harp_rmsnorm_q8(x, weight, res)
+            wait()
+            y = layers[0](q, s)
+            wait()
+            q = rope.append(cache, y.view(seqs, heads, hd), kv_in[:, :kv], kv_in[:, kv:], pos, table)
+            wait()
+            o = rb.harp_paged_attention(q, cache, table, lens)
+            wait()
+            x = layers[1](*rb.harp_quantize_q8(o.view(seqs, width)))
+            wait()
+            out.append(x)
+        return torch.stack(out)
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        got = chain(lambda: None)
+        assert torch.equal(got, want)
+    clean(rb)
+
+
+def test_calls_on_two_streams_do_not_disturb_each_other(rb):
+    g = gen(37)
+    q, cache, table, n = attention_case(rb, [700, 31, 0, 2000], 16, 4, 128, 16, torch.bfloat16)
+    x, sx, w, sw = linear_case(rb, 300, 1024, 2048)
+    layer = rb.HarpLinear8(w, sw)
+    a0, y0 = rb.harp_paged_attention(q, cache, table, n), layer(x, sx)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append((rb.harp_paged_attention(q, cache, table, n), layer(x, sx)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, a0) and torch.equal(y, y0) for a, y in got)
+    clean(rb)
+
+
+def test_linear8_refuses_what_it_cannot_count(rb):
+    codes = torch.zeros(128, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    layer = rb.HarpLinear8(codes, torch.ones(1, 1, device="cuda"))
+    with pytest.raises(ValueError):
+        layer(torch.zeros(2, 63, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn), torch.ones(2, 1, device="cuda"))
+    with pytest.raises(ValueError):
+        layer(codes, torch.ones(127, 1, device="cuda"))
+    with pytest.raises(ValueError):
+        layer(codes, torch.ones(128, 1, device="cuda"), out=torch.empty(128, 127, device="cuda"))
+    layer.close()
+    with pytest.raises(rb.HarpError):
+        layer(codes, torch.ones(128, 1, device="cuda"))
+
+
 def stack_case(rb, hidden, ffn, nh, nkv, hd, blocks, wb):
     from harp_cases import device_layer, oracle_layer
     shapes = [(nh * hd, hidden), (nkv * hd, hidden), (nkv * hd, hidden), (hidden, nh * hd), (ffn, hidden), (ffn, hidden), (hidden, ffn)]
