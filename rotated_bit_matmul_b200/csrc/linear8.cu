@@ -177,8 +177,21 @@ struct Bars {
   uint64_t accempty[kMaxAcc];
   uint64_t scale[kMaxSlots];
   uint32_t tslot;
+  uint32_t lost;             // some wait ran out
+  uint32_t copied, issued;   // K steps whose copies, whose MMAs were asked for
 };
 static_assert(sizeof(Bars) <= 1024, "barriers");
+
+__device__ __forceinline__ void note_lost(Bars* bars) { *reinterpret_cast<volatile uint32_t*>(&bars->lost) = 1; }
+// After a wait has run out (one thread, all others past their work): what was asked for lands
+// before the CTA may leave. Otherwise the summing warps have waited for everything already, and
+// nothing is tried again: 22 tries at the end of every call cost 4000 cycles.
+__device__ __noinline__ void drain(Bars* bars, int stages, int slots, int* status, uint64_t limit_ns) {
+  const int c = (int)bars->copied, m = (int)bars->issued;
+  for (int q = max(0, c - stages); q < c; ++q) mbar_wait(&bars->full[q % stages], (q / stages) & 1, status, 101, limit_ns);
+  for (int q = slots ? max(0, c - slots) : c; q < c; ++q) mbar_wait(&bars->scale[q % slots], (q / slots) & 1, status, 102, limit_ns);
+  for (int q = max(0, m - stages); q < m; ++q) mbar_wait(&bars->done[q % stages], (q / stages) & 1, status, 105, limit_ns);
+}
 
 // tile i of the launch: token tiles of 8 consecutive weight tiles together, so that a wave of
 // CTAs reads few distinct operand tiles
@@ -214,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
       mbar_init(&bars->accempty[i], kSumWarps);
     }
     for (int i = 0; i < SL; ++i) mbar_init(&bars->scale[i], 1);
+    bars->lost = 0;
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -261,10 +275,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
           bulk_g2s(scale_s + (k % SL) * BT, p.sx + (int64_t)kb * p.sx_ld + (int64_t)tt * BT, sbytes, sb);
         }
       }
-      // copies still in flight land before the CTA may leave
-      for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->full[q % ST], (q / ST) & 1, p.status, 101, p.wait_ns);
-      for (int q = max(0, k - SL); q < k; ++q)
-        mbar_wait(&bars->scale[q % SL], (q / SL) & 1, p.status, 102, p.wait_ns);
+      bars->copied = (uint32_t)k;
+      if (!ok) note_lost(bars);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -294,9 +306,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
           turn ^= 1;
         }
       }
-    // the MMAs in flight end before tensor memory is freed
-    if (lane == 0)
-      for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->done[q % ST], (q / ST) & 1, p.status, 105, p.wait_ns);
+    if (lane == 0) {
+      bars->issued = (uint32_t)k;
+      if (!ok) note_lost(bars);
+    }
     __syncwarp();
   } else {
     // ---------------- scaled sums: thread = weight row, half the tile's tokens
@@ -326,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
         }
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
+          if (lane == 0) note_lost(bars);
           break;
         }
         tc_fence_after();
@@ -383,6 +397,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
   }
   tc_fence_before();
   __syncthreads();
+  if (bars->lost) {  // uniform: nothing writes it any more
+    if (tid == 0) drain(bars, ST, SL, p.status, p.wait_ns);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
@@ -462,6 +480,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->done[i], 1);
     }
+    bars->lost = 0;
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -502,7 +521,8 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
           }
         }
       }
-      for (int q = max(0, k - ST); q < k; ++q) mbar_wait(&bars->full[q % ST], (q / ST) & 1, p.status, 101, p.wait_ns);
+      bars->copied = (uint32_t)k;
+      if (!ok) note_lost(bars);
     } else if (warp == 1) {
       // ---------------- MMA issuer: the whole warp walks the steps, so that descriptors and
       // addresses stay warp-uniform, and one lane issues. A step whose wait ran out is not issued;
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
       const uint32_t idesc = idesc_e4m3(kBM, BN);
       const uint64_t a0 = sw128_desc(smem_u32(ring)), w0 = sw128_desc(smem_u32(ring) + kBM * kBK);
       const bool leader = elect_lane();
-      int k = 0, slot = 0;
+      int k = 0, slot = 0, issued = 0;
       uint32_t turn = 0;
       bool ok = true;
       for (int i = blockIdx.x; i < tiles; i += gridDim.x)
@@ -528,6 +548,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
               mma_commit(&bars->done[slot]);
             }
             __syncwarp();
+            issued = k + 1;
           }
           if (++slot == ST) {
             slot = 0;
@@ -535,6 +556,10 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
           }
         }
       for (int q = max(0, k - C::kAcc); q < k; ++q) bar_sync(kBarFree + q % C::kAcc, C::kBarThreads);
+      if (lane == 0) {
+        bars->issued = (uint32_t)(ok ? k : issued);
+        if (!ok) note_lost(bars);
+      }
     } else if (warp == 2) {
       // ---------------- relay: waits for the MMAs of a step and lets the summing warps go
       int k = 0, slot = 0;
@@ -549,6 +574,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
             turn ^= 1;
           }
         }
+      if (!ok && lane == 0) note_lost(bars);
     }
     __syncwarp();
   } else {
@@ -661,6 +687,10 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
   }
   tc_fence_before();
   __syncthreads();
+  if (bars->lost) {  // uniform: nothing writes it any more
+    if (tid == 0) drain(bars, ST, 0, p.status, p.wait_ns);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
