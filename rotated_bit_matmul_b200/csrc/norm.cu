@@ -4,11 +4,13 @@
 //   h = x + r,   y = h / sqrt(mean(h^2) + eps) * w,
 //   8-bit output: s = max |y| / 448 over 128 columns (1 where that is 0), q = e4m3(y / s).
 //
+// The codes do not depend on the norm: with a = h w, y / s = 448 a / max |a|. So q is taken
+// from a and its maximum, in fp32, and again in fp64 for the few values whose fp32 quotient lies
+// within its error of the middle between two codes. s is stored rounded to fp32.
+//
 // One pass: a row's values are loaded once and stay in registers between the sum of squares
 // and the output, so the kernel moves what the formula needs and no more. The sum of squares
-// is fp32 (a thread's few values, then a fixed tree), and y / s is good to a few units, so that
-// a code differs from the exact one only where y / s lies within fp32 rounding of the border
-// between two codes.
+// is fp32 (a thread's few values, then a fixed tree).
 //
 // Two mappings of a row onto threads:
 //   * rows that start on 16-byte boundaries: a thread holds 8 consecutive columns per step
@@ -55,21 +57,55 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-__device__ __forceinline__ float block_scale(float amax) {
-  const float s = amax / 448.f;
-  return s == 0.f ? 1.f : s;
+// What a block of columns is multiplied by before its rounding to e4m3, and its scale: `amax` is
+// the largest |a|, a * inv the value to be held. NaN anywhere makes both NaN; where the scale
+// comes out as 0 it is 1 and every code 0.
+struct Block {
+  float amax, scale, factor;
+};
+__device__ __forceinline__ Block block_of(float amax, float inv) {
+  Block b;
+  b.amax = amax;
+  b.scale = amax * inv / 448.f;
+  b.factor = 448.f / amax;
+  if (b.scale == 0.f) {
+    b.scale = 1.f;
+    b.factor = 0.f;
+  } else if (!(b.scale == b.scale)) {
+    b.factor = b.scale;
+  }
+  return b;
 }
-
-// v / s: times 1 / s (rounded twice, within 1.5 units), divided where 1 / s would overflow
+// a * 448 / amax, so that its rounding to e4m3 is that of the exact quotient. The fp32 product v
+// is off by at most one unit (the factor and v rounded once each): where v is within 2 units of
+// the middle between two codes (its 20 bits behind e4m3's three are near 0x80000), the quotient
+// is taken in fp64 and rounded to fp32 by truncation with a sticky last bit, which no later
+// rounding to fewer bits mistakes. `near` is at most kNear there: two instructions per value, and
+// a branch that 5 of 2^20 values take (8192 x 8192 bf16: 75 us without, 79 with it; the
+// products of h and w are rounded, and e4m3's denormals, whose middles lie elsewhere, are left
+// to fp32).
+constexpr uint32_t kNear = 4u << 12;
+__device__ __forceinline__ uint32_t near_middle(float v) { return __float_as_uint(v) * 4096u + (0x80002u << 12); }
+__device__ __forceinline__ float exact_quotient(float a, double factor) {
+  const double d = (double)a * factor;
+  const float f = __double2float_rz(d);
+  return (double)f == d ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+// v * b.factor for N values of a block
 template <int N>
-__device__ __forceinline__ void over_scale(const float (&v)[N], float s, float (&d)[N]) {
-  if (s >= 0x1p-120f || !(s == s)) {
-    const float r = 1.f / s;
+__device__ __forceinline__ void quotients(const Block& b, const float (&a)[N], float (&q)[N]) {
+  uint32_t near = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = v[i] * r;
-  } else {
+  for (int i = 0; i < N; ++i) {
+    q[i] = a[i] * b.factor;
+    near = min(near, near_middle(q[i]));
+  }
+  if (near <= kNear) {
+    // one Newton step on the fp32 quotient: 448 / amax to 2^-46
+    const double f0 = b.factor, factor = fma(fma(-f0, (double)b.amax, 448.0), f0 * (1.0 / 448.0), f0);
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = v[i] / s;
+    for (int i = 0; i < N; ++i)
+      if (near_middle(q[i]) <= kNear) q[i] = exact_quotient(a[i], factor);
   }
 }
 
@@ -98,7 +134,7 @@ __device__ __forceinline__ float inv_rms(float sum, int n, float eps) { return 1
 constexpr int kNone = -1;
 
 template <int XT, int RT, int STEPS, bool Q8>
-__global__ void __launch_bounds__(STEPS == 1 ? 1024 : 512) norm_vec_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(STEPS == 1 ? 1024 : 512, STEPS == 4 ? 2 : 1) norm_vec_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[32];
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int tx = threadIdx.x, T = blockDim.x;
@@ -148,71 +184,67 @@ __global__ void __launch_bounds__(STEPS == 1 ? 1024 : 512) norm_vec_kernel(const
         for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.h, ho + c + i, RT, v[k][i]);
     }
   }
+  float inv = 1.f;
   if (p.norm) {
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(v[k][i], v[k][i], s);
-    const float inv = inv_rms(row_sum(s, red), n, p.eps);
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] *= inv;
-    if (p.w) {
-      auto weigh = [&](int wt) {
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-          const int c = (k * T + tx) * 8;
-          if (c + 8 <= n) {
-            float t[8];
-            raw_unpack8(raw_load8(p.w, c, wt), wt, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] *= t[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + i < n) v[k][i] *= load_act(p.w, c + i, wt);
-          }
-        }
-      };
-      if (p.wt == XT) weigh(XT);  // the usual case without a branch per step
-      else weigh(p.wt);
-    }
+    inv = inv_rms(row_sum(s, red), n, p.eps);
   }
   const int64_t yo = row * p.ys;
+  auto finish = [&](int wt) {  // wt: the weight's type, or kNone
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    const int c = (k * T + tx) * 8;
-    if (Q8) {
-      float amax = 0.f;
+    for (int k = 0; k < STEPS; ++k) {
+      const int c = (k * T + tx) * 8;
+      if (!Q8) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(v[k][i]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float s = block_scale(amax);
-      if (c < n) {
-        if ((tx & 15) == 0) p.scale[(int64_t)(c / kBlk) * p.scale_ld + row] = s;
-        uint8_t* q = static_cast<uint8_t*>(p.y) + yo + c;
-        float d[8];
-        over_scale(v[k], s, d);
-        uint32_t w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(d[4 * j], d[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(d[4 * j + 2], d[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
-          w[j] = lo | (hi << 16);
-        }
-        if (c + 8 <= n) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-        else
-          for (int i = 0; i < 8 && c + i < n; ++i) q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; i < 8; ++i) v[k][i] *= inv;
       }
-    } else {
-      if (c + 8 <= n) store8(p.y, yo + c, p.yt, v[k]);
-      else
-        for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.y, yo + c + i, p.yt, v[k][i]);
+      if (wt != kNone) {
+        float w[8];
+        if (c + 8 <= n) {
+          raw_unpack8(raw_load8(p.w, c, wt), wt, w);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = c + i < n ? load_act(p.w, c + i, wt) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] *= w[i];
+      }
+      if (Q8) {
+        float amax = 0.f, a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(v[k][i]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const Block blk = block_of(amax, inv);
+        if (c < n) {
+          if ((tx & 15) == 0) p.scale[(int64_t)(c / kBlk) * p.scale_ld + row] = blk.scale;
+          uint8_t* q = static_cast<uint8_t*>(p.y) + yo + c;
+          quotients(blk, v[k], a);
+          uint32_t o[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a[4 * j], a[4 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(a[4 * j + 2], a[4 * j + 3]), __NV_SATFINITE, __NV_E4M3);
+            o[j] = lo | (hi << 16);
+          }
+          if (c + 8 <= n) *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
+          else
+            for (int i = 0; i < 8 && c + i < n; ++i) q[i] = (uint8_t)(o[i >> 2] >> (8 * (i & 3)));
+        }
+      } else {
+        if (c + 8 <= n) store8(p.y, yo + c, p.yt, v[k]);
+        else
+          for (int i = 0; i < 8 && c + i < n; ++i) store_act(p.y, yo + c + i, p.yt, v[k][i]);
+      }
     }
-  }
+  };
+  if (!p.w) finish(kNone);
+  else if (p.wt == XT) finish(XT);  // the usual case without a branch per step
+  else finish(p.wt);
 }
 
 // the same for rows at any alignment: a warp per block of 128 columns and step; whole blocks
@@ -255,13 +287,6 @@ __device__ __forceinline__ void take4(const void* base, int64_t at, int left, fl
       v[i] = (ADD ? v[i] : 0.f) + x;
     }
   }
-}
-template <int T>
-__device__ __forceinline__ void weigh4(const void* base, int64_t at, int left, float (&v)[4]) {
-  float w[4];
-  take4<T, false>(base, at, left, w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] *= w[i];  // 0 behind the row, where v is 0 too
 }
 template <int T>
 __device__ __forceinline__ void put4(void* base, int64_t at, int left, const float (&v)[4]) {
@@ -307,44 +332,45 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
       }
     }
   }
+  float inv = 1.f;
   if (p.norm) {
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fmaf(v[k][i], v[k][i], s);
-    const float inv = inv_rms(row_sum(s, red), n, p.eps);
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-      const int c0 = (k * W + warp) * kBlk;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[k][i] *= inv;
-      if (p.w) {
-        if (p.wt == DT_F32) weigh4<DT_F32>(p.w, c0 + lane, n - c0, v[k]);
-        else if (p.wt == DT_BF16) weigh4<DT_BF16>(p.w, c0 + lane, n - c0, v[k]);
-        else weigh4<DT_F16>(p.w, c0 + lane, n - c0, v[k]);
-      }
-    }
+    inv = inv_rms(row_sum(s, red), n, p.eps);
   }
   const int64_t yo = row * p.ys + lane;
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
     const int c0 = (k * W + warp) * kBlk, left = n - c0;
     if (left <= 0) break;  // uniform in the warp
+    if (!Q8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k][i] *= inv;
+    }
+    if (p.w) {  // (0 behind the row, where v is 0 too)
+      float w[4];
+      if (p.wt == DT_F32) take4<DT_F32, false>(p.w, c0 + lane, left, w);
+      else if (p.wt == DT_BF16) take4<DT_BF16, false>(p.w, c0 + lane, left, w);
+      else take4<DT_F16, false>(p.w, c0 + lane, left, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k][i] *= w[i];
+    }
     if (Q8) {
-      float amax = 0.f;
+      float amax = 0.f, a[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) amax = max_nan(amax, fabsf(v[k][i]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float s = block_scale(amax);
-      if (lane == 0) p.scale[(int64_t)(c0 / kBlk) * p.scale_ld + row] = s;
-      float d[4];
-      over_scale(v[k], s, d);
+      const Block blk = block_of(amax, inv);
+      if (lane == 0) p.scale[(int64_t)(c0 / kBlk) * p.scale_ld + row] = blk.scale;
+      quotients(blk, v[k], a);
       uint8_t* q = static_cast<uint8_t*>(p.y) + yo + c0;
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(d[i], d[i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(a[i], a[i + 1]), __NV_SATFINITE, __NV_E4M3);
         if (left >= kBlk || lane + 32 * i < left) q[32 * i] = (uint8_t)two;
         if (left >= kBlk || lane + 32 * (i + 1) < left) q[32 * (i + 1)] = (uint8_t)(two >> 8);
       }
@@ -383,13 +409,13 @@ __global__ void __launch_bounds__(256) weights_q8_kernel(const void* w, int wt, 
   amax = red[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) amax = max_nan(amax, red[i]);
-  const float s = block_scale(amax);
-  if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * kblocks + blockIdx.x] = s;
+  const Block blk = block_of(amax, 1.f);
+  if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * kblocks + blockIdx.x] = blk.scale;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int64_t r = r0 + tr + 16 * k;
     float d[8];
-    over_scale(v[k], s, d);
+    quotients(blk, v[k], d);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t c = c0 + tc + i;
@@ -411,7 +437,7 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
   // Few rows: as many threads as the row has work for, for latency. Many: four steps per thread
   // where the row has them, one warp per row up to 1024 columns, so that an SM holds
   // many rows and one row's sum hides behind another's loads (8192 x 8192 bf16 with a residual:
-  // one step 179 us, four 84).
+  // one step 179 us, four 79).
   int steps = 1;
   if (p.rows > 2 * 148)
     while (steps < (!vec && warps <= 8 ? 8 : 4) && warps > steps) steps *= 2;
