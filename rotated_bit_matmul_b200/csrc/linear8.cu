@@ -705,13 +705,14 @@ struct Plan {
 
 // Up to 128 tokens, or too few 128 x 128 tiles to fill the GPU: few_kernel with the narrowest
 // tile that holds the tokens (64 at most), cut over K while all CTAs fit on the GPU at once
-// (two per SM), each over at least 4 K steps. Else many_kernel, 192 wide unless 128 takes fewer
-// waves x width.
+// (two per SM), each over at least 4 K steps. Else many_kernel, 192 wide unless 128 takes no more
+// waves: a step of 128 rows takes some 0.85 of the time of one of 192 (256 x 8192 x 8192, one wave
+// of either: 25 us with 128, 27 with 192; 1024 x 8192 x 8192, 4 waves against 3: 84 and 73).
 Plan choose(int64_t tokens, int64_t n_out, int kblocks) {
   auto tiles = [&](int64_t w, int64_t t) { return ((n_out + w - 1) / w) * ((tokens + t - 1) / t); };
   if (tokens > 128 && tiles(128, 128) >= 100) {
-    const int64_t w192 = (tiles(192, 128) + 147) / 148 * 192, w128 = (tiles(128, 128) + 147) / 148 * 192;
-    return Plan{true, w128 < w192 ? 128 : 192, 1};
+    auto waves = [&](int64_t w) { return (tiles(w, 128) + 147) / 148; };
+    return Plan{true, waves(128) <= waves(192) ? 128 : 192, 1};
   }
   Plan best{false, tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, 1};
   const int64_t n = tiles(kBM, best.width);
