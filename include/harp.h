@@ -72,11 +72,12 @@ harp_status harp_device_status(void* stream);
 
 /* Testing hook for the failure paths; everything is off by default and the paper has no
  * counterpart. It applies process-wide to launches made after it:
- *   wait_limit_us   : > 0 bounds the device-side waits of harp_linear_fwd's dequant-GEMV and of
- *                     the fused decode step by that many microseconds (0 restores the default,
- *                     about 1-2 s);
+ *   wait_limit_us   : > 0 bounds the device-side waits of harp_linear_fwd's dequant-GEMV, of the
+ *                     fused decode step, of harp_linear8_fwd and of harp_paged_attention by
+ *                     about that many microseconds (0 restores the default, about 1-2 s);
  *   gemv_skip_stage : >= 0 makes the first CTA of the dequant-GEMV skip issuing that stage of
- *                     its weight ring, so its consumers' wait runs out (-1: off);
+ *                     its weight ring, and that of harp_linear8_fwd that K step and those
+ *                     after it, so its consumers' wait runs out (-1: off);
  *   decode_barrier  : >= 0 raises the arrival target of that grid barrier of the fused decode
  *                     step (index 5 * block + phase) by one, so no CTA passes it (-1: off).
  * A wait that runs out records HARP_ERR_TIMEOUT and its site in the device status word and
@@ -443,7 +444,8 @@ harp_status harp_rope_apply(harp_rope rope, int64_t tokens, int heads, const int
  * lies in page page_table[s * max_pages + j / page_size], row j % page_size.
  * dtype bf16 or f16; page_size a power of two, at most 4096; head_dim even, at most 256; strides
  * positive multiples of 8; k and v 16-byte aligned. Page indices outside [0, n_pages) are never
- * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93; 95, 96: HARP_ERR_TIMEOUT of a copy) and takes their rows as 0. */
+ * followed: the kernel reports HARP_ERR_DEVICE_CHECK (sites 90-93; 95, 96: HARP_ERR_TIMEOUT of a copy) and takes their
+ * rows as 0. */
 typedef struct {
   void* k;
   void* v;

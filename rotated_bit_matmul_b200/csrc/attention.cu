@@ -56,6 +56,7 @@ struct Params {
   int tile_shift;  // log2 keys per tile
   int pair_cost;
   int box_rows;    // rows of a TMA box: the page size, at most 16
+  uint64_t wait_ns;
   int page_shift;
   float scale_log2;
   float* part_o;   // [workers][2][kRows][head_dim]: [0] of the pair that began in an earlier
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
 
     for (int tile = use.tile; tile < use.stop; ++tile) {
       if (ok) {
-        ok = mbar_wait_warp(&full[slot], phase, c.status, 95, 1000000000ull);
+        ok = mbar_wait_warp(&full[slot], phase, c.status, 95, p.wait_ns);
         if (ok) {
           --in_flight;
         } else {  // reported: ask for nothing more and run to the end
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
   }
   if (!ok)  // copies still in flight land before the CTA may leave
     for (; in_flight > 0; --in_flight) {
-      mbar_wait(&full[lost_slot], lost_phase, c.status, 96);
+      mbar_wait(&full[lost_slot], lost_phase, c.status, 96, p.wait_ns);
       if (++lost_slot == ST) {
         lost_slot = 0;
         lost_phase ^= 1;
@@ -800,6 +801,7 @@ cudaError_t launch_attention(const AttnCall& c, cudaStream_t st) {
   while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
   p.scale_log2 = c.scale * 1.44269504088896340736f;
   p.box_rows = std::min(c.page_size, kWarpKeys);
+  p.wait_ns = test_hooks().wait_ns;
   const uint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.page_size, (uint64_t)c.n_kv, (uint64_t)c.n_pages};
   const uint64_t strides[3] = {2 * (uint64_t)c.row_stride, 2 * (uint64_t)c.head_stride, 2 * (uint64_t)c.page_stride};
   const uint32_t box[4] = {64, (uint32_t)p.box_rows, 1, 1};

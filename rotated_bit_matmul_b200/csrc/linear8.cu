@@ -27,6 +27,7 @@
 #include "serve.h"
 
 #include <algorithm>
+#include <climits>
 #include <new>
 
 namespace harp {
@@ -155,6 +156,7 @@ struct Params {
   int64_t ys;
   int* status;
   uint64_t wait_ns;
+  int stop;                // testing hook: K step from which CTA 0 asks for no copies
 };
 
 template <int BT>
@@ -251,13 +253,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
   if (warp == 0) {
     // ---------------- producer
     if (lane == 0) {
+      const int stop = blockIdx.x == 0 ? p.stop : INT_MAX;
       int k = 0;  // K steps of this CTA so far, over all its tiles
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
         int nt, tt;
         tile_at(p, i, nt, tt);
         const uint32_t sbytes = (uint32_t)(min(BT, (p.tokens - tt * BT + 3) & ~3) * 4);
-        for (int kb = kb0; kb < kb1; ++kb, ++k) {
+        for (int kb = kb0, end = kb0 + min(nkb, stop - k); kb < end; ++kb, ++k) {
           const int slot = k % ST;
           if (k >= ST && !mbar_wait_lane(&bars->done[slot], ((k / ST) - 1) & 1, p.status, 100, p.wait_ns)) {
             ok = false;
@@ -435,9 +438,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BT>::kPerSm) few_kernel(const __
 // (4096 x 8192 x 28672: 0.94 ms; pairs of CTAs with the M = 256 MMA, whose hand-offs cross the
 // pair, 1.01 ms). So a relay warp waits for the MMAs, and it and the issuer meet the summing
 // warps at named barriers, which are not in shared memory. Barrier kBarReady + b: accumulator b
-// is complete; kBarFree + b: it has been read. Neither can be passed twice by one side: the
-// next step of an accumulator needs the other side first.
-constexpr int kBarReady = 1, kBarFree = 5;
+// is complete; kBarFree + b: it has been read; kBarStep + b: the issuer has been at the step.
+// None can be reached twice by one side before the other has passed it, and this does not rest
+// on the mbarriers, whose waits may run out: the issuer comes to step k + kAcc after step k has
+// been read, the relay to Ready of step k + kAcc after the issuer has been at that step, and
+// the summing warps to its Free after Ready. So every named barrier is passed once per step,
+// lost or not, and the kernel ends.
+constexpr int kBarReady = 1, kBarFree = 5, kBarStep = 9;
 template <int BN>
 struct Many {
   static constexpr int kSums = BN / 64 * 4;
@@ -500,13 +507,15 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
     if (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLow));
     if (warp == 0 && lane == 0) {
       // ---------------- producer
+      const int stop = blockIdx.x == 0 ? p.stop : INT_MAX;
       int k = 0, slot = 0;
       uint32_t turn = 1;  // parity of the phase before the slot's next one
       bool ok = true;
       for (int i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
         int nt, tt;
         tile_at(p, i, nt, tt);
-        for (int kb = 0; kb < nkb; ++kb, ++k) {
+        const int end = min(nkb, stop - k);  // (a test of every step cost 1.5 %)
+        for (int kb = 0; kb < end; ++kb, ++k) {
           if (k >= ST && !mbar_wait_lane(&bars->done[slot], turn, p.status, 100, p.wait_ns)) {
             ok = false;
             break;
@@ -550,6 +559,7 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
             __syncwarp();
             issued = k + 1;
           }
+          bar_arrive(kBarStep + b, 64);
           if (++slot == ST) {
             slot = 0;
             turn ^= 1;
@@ -567,8 +577,10 @@ __global__ void __launch_bounds__(Many<BN>::kThr, 1) many_kernel(const __grid_co
       bool ok = true;
       for (int i = blockIdx.x; i < tiles; i += gridDim.x)
         for (int kb = 0; kb < nkb; ++kb, ++k) {
+          const int b = k % C::kAcc;
+          bar_sync(kBarStep + b, 64);
           ok = ok && __all_sync(0xffffffffu, mbar_wait_spin(&bars->done[slot], turn, p.status, 107, p.wait_ns));
-          bar_arrive(kBarReady + k % C::kAcc, C::kBarThreads);
+          bar_arrive(kBarReady + b, C::kBarThreads);
           if (++slot == ST) {
             slot = 0;
             turn ^= 1;
@@ -860,7 +872,9 @@ harp_status harp_linear8_fwd(harp_layer8 L, int64_t tokens, const void* x, int64
   p.y = y;
   p.yt = yt;
   p.ys = y_stride;
-  p.wait_ns = test_hooks().wait_ns;
+  const TestHooks hooks = test_hooks();
+  p.wait_ns = hooks.wait_ns;
+  p.stop = hooks.gemv_skip_stage < 0 ? INT_MAX : hooks.gemv_skip_stage;
   p.tm_w = nw == 192 ? L->tm_w192 : L->tm_w;
   if (!encode_map_2d(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, (uint64_t)L->n_in, (uint64_t)tokens, (uint64_t)x_stride,
                      l8::kBK, (uint32_t)tw, CU_TENSOR_MAP_SWIZZLE_128B))

@@ -793,3 +793,24 @@ def test_stack_step_cached_first_token_and_padding(rb):
         S.step_cached(x, rope, rb.HarpCache.empty(2, 4, 1, 16, 64, torch.float16), pos, table)
     clean(rb)
     S.close()
+
+
+@pytest.mark.parametrize("tokens,n_out,step", [(3, 256, 0), (3, 256, 3), (20, 4096, 1), (300, 8192, 2), (300, 8001, 9)])
+def test_linear8_wait_that_runs_out(rb, tokens, n_out, step):
+    """The testing hook leaves the copies out from a K step on, under a 1 ms limit: the call ends, the status
+    word says so, and the next call on the device is right."""
+    x, sx, w, sw = linear_case(rb, tokens, 2048, n_out)
+    layer = rb.HarpLinear8(w, sw)
+    want = layer(x, sx, out_dtype=torch.float32)
+    clean(rb)
+    rb.harp_test_set_faults(wait_limit_us=1000, gemv_skip_stage=step)
+    try:
+        layer(x, sx)
+        torch.cuda.synchronize()
+        with pytest.raises(rb.HarpError) as e:
+            rb.harp_device_status()
+    finally:
+        rb.harp_test_set_faults()
+    assert e.value.status == 5 and any(f"site {site}" in str(e.value) for site in range(100, 108)), e.value
+    assert torch.equal(layer(x, sx, out_dtype=torch.float32), want)
+    clean(rb)
