@@ -372,7 +372,8 @@ class HarpStack:
         ws = workspace if workspace is not None else self.cached_workspace(batch)
         with torch.cuda.device(x.device):
             call("harp_stack_step_cached", self.handle, batch, _p(x2), _dt(x2), _p(out), _dt(out), rope._h,
-                 cache.layer(0), cache.layer_stride, _p(positions), _p(page_table), page_table.shape[1], int(window),
+                 cache.layer(0), cache.layer_stride, _p(positions), _p(page_table), page_table.shape[1],
+                 max(-1, min(int(window), 2**31 - 1)),
                  _p(ws), ws.numel(), _stream())
         return out
 

@@ -17,6 +17,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <optional>
 #include <string>
@@ -417,7 +418,7 @@ PyObject* paged_attention(PyObject* const* a, Py_ssize_t n) {
     if (!ws.is_contiguous()) throw Refused{"workspace must be contiguous"};
     settle(f_attention(cache, (int)m, (int)heads, q.data_ptr(), q.stride(0), q.stride(1), static_cast<const int32_t*>(table.data_ptr()),
                        table.size(1), static_cast<const int32_t*>(lens.data_ptr()),
-                       a[5] == Py_None ? 1.0f / std::sqrt((float)hd) : (float)real(a[5]), (int)whole(a[6]), y.data_ptr(), y.stride(0),
+                       a[5] == Py_None ? 1.0f / std::sqrt((float)hd) : (float)real(a[5]), (int)std::clamp<int64_t>(whole(a[6]), -1, 0x7fffffff), y.data_ptr(), y.stride(0),
                        y.stride(1), static_cast<float*>(ptr(lse)), ws.data_ptr(), ws.nbytes(), stream_of(dev.index)),
            "harp_paged_attention");
   }

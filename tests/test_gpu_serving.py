@@ -814,3 +814,14 @@ def test_linear8_wait_that_runs_out(rb, tokens, n_out, step):
     assert e.value.status == 5 and any(f"site {site}" in str(e.value) for site in range(100, 108)), e.value
     assert torch.equal(layer(x, sx, out_dtype=torch.float32), want)
     clean(rb)
+
+
+def test_paged_attention_windows_of_any_size(rb):
+    q, cache, table, n = attention_case(rb, [100, 50], 4, 2, 64, 16, torch.bfloat16)
+    full = rb.harp_paged_attention(q, cache, table, n)
+    for window in (100, 2**31 - 1, 2**31, 2**40):
+        assert torch.equal(rb.harp_paged_attention(q, cache, table, n, window=window), full)
+    for window in (-1, -2**40):
+        with pytest.raises(rb.HarpError):
+            rb.harp_paged_attention(q, cache, table, n, window=window)
+    clean(rb)
