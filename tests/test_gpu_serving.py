@@ -816,6 +816,48 @@ def test_linear8_wait_that_runs_out(rb, tokens, n_out, step):
     clean(rb)
 
 
+def test_served_token_with_an_8_bit_head(rb):
+    """A cached step of the stack, the last norm with its 8-bit output and the head, captured as one
+    graph: logits within the codes' half steps of the same chain in fp64 from the step's output."""
+    ol, layers, S = stack_case(rb, 256, 768, 4, 2, 64, 2, 256)
+    g = gen(41)
+    cache = rb.HarpCache.empty(2, 8, 2, 16, 64)
+    rope = rb.HarpRope(64)
+    weight = 1 + 0.1 * randn(g, 256)
+    W = randn(g, 1000, 256) / 16
+    head = rb.HarpLinear8(*rb.harp_quantize_weights_q8(W))
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = randn(g, 2, 256)
+    ws = S.cached_workspace(2)
+
+    def token():
+        h = S.step_cached(x, rope, cache, pos, table, workspace=ws)
+        return h, head(*rb.harp_rmsnorm_q8(h, weight=weight), out_dtype=torch.float32)
+
+    token()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, logits = token()
+    for t in range(20):
+        x.copy_(randn(g, 2, 256))
+        pos.fill_(t)
+        graph.replay()
+        eager_h, eager = token()  # writes the same cache rows again
+        assert torch.equal(h, eager_h) and torch.equal(logits, eager)
+        y = norm64(h, weight, None, 1e-5)[1]
+        want = y @ W.double().t()
+        # codes: half a step (2^-4) of a value each, or 2^-10 of the block's 448th; products of two
+        # such errors, and their sum over the columns
+        ey = y.abs() * 2.0**-4 + y.abs().amax(-1, keepdim=True) / 448 * 2.0**-10
+        eW = W.double().abs() * 2.0**-4 + W.double().abs().amax() / 448 * 2.0**-10
+        tol = ey @ W.double().abs().t() + y.abs() @ eW.t() + ey @ eW.t()
+        close(logits, want, tol * (1 + 1e-3))
+    clean(rb)
+    S.close()
+
+
 def test_paged_attention_windows_of_any_size(rb):
     q, cache, table, n = attention_case(rb, [100, 50], 4, 2, 64, 16, torch.bfloat16)
     full = rb.harp_paged_attention(q, cache, table, n)
