@@ -833,7 +833,7 @@ harp_status harp_paged_attention(const harp_kv_cache* cache, int n_seqs, int n_h
   if (!q || !page_table || !seq_lens || !out) return set_error(HARP_ERR_INVALID_ARG, "paged_attention: null pointer");
   if (const char* why = attention_refuses(n_seqs, n_heads, cache->n_kv_heads, cache->head_dim, cache->dtype))
     return set_error(why[0] == 'h' ? HARP_ERR_UNSUPPORTED : HARP_ERR_INVALID_ARG, "paged_attention: %s", why);
-  if (max_pages < 1 || max_pages * cache->page_size > 0x7fffff00) return set_error(HARP_ERR_INVALID_ARG, "paged_attention: max_pages out of range");
+  if (max_pages < 1 || max_pages > 0x7fffff00 / cache->page_size) return set_error(HARP_ERR_INVALID_ARG, "paged_attention: max_pages out of range");
   if (window < 0 || !(scale == scale)) return set_error(HARP_ERR_INVALID_ARG, "paged_attention: bad scale or window");
   if (!aligned_to(q, 4) || !aligned_to(out, 4) || (q_seq_stride | q_head_stride | o_seq_stride | o_head_stride) & 1)
     return set_error(HARP_ERR_INVALID_ARG, "paged_attention: rows of q and out must lie on 4-byte boundaries");

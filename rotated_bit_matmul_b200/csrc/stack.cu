@@ -568,7 +568,7 @@ harp_status harp_stack_step_cached(harp_stack S, int batch, const void* x, harp_
     return sfail(HARP_ERR_UNSUPPORTED, std::string("stack_step_cached: ") + why);
   if (layer_stride < 0 || layer_stride % 8 || (S->n_layers > 1 && layer_stride == 0))
     return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: layer_stride must be a positive multiple of 8");
-  if (max_pages < 1 || max_pages * cache->page_size > 0x7fffff00 || window < 0)
+  if (max_pages < 1 || max_pages > 0x7fffff00 / cache->page_size || window < 0)
     return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: max_pages or window out of range");
   if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(page_table)) & 3u)
     return sfail(HARP_ERR_INVALID_ARG, "stack_step_cached: positions and page_table must be 4-byte aligned");

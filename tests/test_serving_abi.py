@@ -173,6 +173,8 @@ def test_paged_attention_refusals(lib):
                     (dict(bytes=n.value - 1), WORKSPACE)):
         assert lib.harp_paged_attention(*_changed(A, **kw)) == err, kw
     assert lib.harp_paged_attention(*_changed(A, seqs=0)) == 0
+    for pages in (1 << 60, (1 << 63) - 1):  # rows beyond 64 bits
+        assert lib.harp_paged_attention(*_changed(A, pages=pages)) == INVALID
     for hd, err in ((40, UNSUPPORTED), (80, UNSUPPORTED), (224, UNSUPPORTED)):
         d = _cache(head_dim=hd, row_stride=hd)
         assert lib.harp_paged_attention(*_changed(A, cache=ctypes.byref(d), bytes=1 << 40)) == err
