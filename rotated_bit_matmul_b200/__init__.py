@@ -369,12 +369,15 @@ class HarpStack:
             raise ValueError(f"page_table must be contiguous int32 [{batch}, pages]")
         if out is None:
             out = torch.empty(x2.shape, dtype=out_dtype or torch.float32, device=x.device)
+        elif out.numel() != x2.numel() or out.shape[-1] != self.hidden or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous with {batch} rows of {self.hidden}")
+        if any(t is not None and t.device != x.device for t in (positions, page_table, cache.k, out, workspace)):
+            raise ValueError("rotated_bit_matmul_b200 works on CUDA tensors of one device only")
         ws = workspace if workspace is not None else self.cached_workspace(batch)
         with torch.cuda.device(x.device):
             call("harp_stack_step_cached", self.handle, batch, _p(x2), _dt(x2), _p(out), _dt(out), rope._h,
                  cache.layer(0), cache.layer_stride, _p(positions), _p(page_table), page_table.shape[1],
-                 max(-1, min(int(window), 2**31 - 1)),
-                 _p(ws), ws.numel(), _stream())
+                 max(-1, min(int(window), 2**31 - 1)), _p(ws), ws.numel(), _stream())
         return out
 
     def close(self):

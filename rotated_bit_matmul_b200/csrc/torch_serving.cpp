@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -322,6 +323,14 @@ at::Tensor heads_of(const at::Tensor& t, const char* what) {
   return t.stride(2) == 1 || t.size(2) == 1 ? t : t.contiguous();
 }
 
+// an output of heads that the caller passed
+void head_target(const std::optional<at::Tensor>& out, at::IntArrayRef shape) {
+  if (!out) return;
+  if (out->sizes() != shape || (out->stride(2) != 1 && out->size(2) > 1))
+    throw Refused{"out must have the input's shape with a contiguous head_dim"};
+  if (at::has_internal_overlap(*out) == at::MemOverlap::Yes) throw Refused{"rows of out lie over one another"};
+}
+
 // handle, head_dim, x, positions, inverse, out_dtype, out
 PyObject* rope_apply(PyObject* const* a, Py_ssize_t n) {
   need(n, 7);
@@ -333,7 +342,7 @@ PyObject* rope_apply(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor x = heads_of(x0, "x"), p = index_of(p0, 1, "positions");
   if (x.size(0) != p.size(0) || x.size(2) != hd)
     throw Refused{"x must be [" + std::to_string(p.size(0)) + ", heads, " + std::to_string(hd) + "]"};
-  if (out && (out->sizes() != x.sizes() || out->stride(2) != 1)) throw Refused{"out must have x's shape with a contiguous head_dim"};
+  head_target(out, x.sizes());
   const harp_dtype xt = type_of(x.scalar_type(), "x");
   const at::Tensor y = out ? *out : empty(x.sizes(), scalar_or(a[5], x.scalar_type()), x);
   const harp_dtype yt = type_of(y.scalar_type(), "out");
@@ -372,7 +381,7 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
     throw Refused{"q must be [" + std::to_string(tokens) + ", heads, " + std::to_string(cache->head_dim) + "], k and v the same with " +
                   std::to_string(cache->n_kv_heads) + " heads"};
   if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type()) throw Refused{"q, k and v must share a dtype"};
-  if (out && (out->sizes() != q.sizes() || out->stride(2) != 1)) throw Refused{"out must have q's shape with a contiguous head_dim"};
+  head_target(out, q.sizes());
   const harp_dtype xt = type_of(q.scalar_type(), "q");
   const at::Tensor y = out ? *out : empty(q.sizes(), scalar_or(a[10], ck.scalar_type()), q);
   const harp_dtype yt = type_of(y.scalar_type(), "out");
@@ -404,8 +413,8 @@ PyObject* paged_attention(PyObject* const* a, Py_ssize_t n) {
     throw Refused{"q, page_table, seq_lens and the cache's head_dim do not match"};
   if (q.scalar_type() != ck.scalar_type()) throw Refused{"q must have the cache's dtype"};
   if ((reinterpret_cast<uintptr_t>(q.data_ptr()) & 3) || (q.stride(0) & 1) || (q.stride(1) & 1)) q = q.clone(at::MemoryFormat::Contiguous);
-  if (out && (out->sizes() != q.sizes() || out->scalar_type() != q.scalar_type() || out->stride(2) != 1))
-    throw Refused{"out must have q's shape and dtype with a contiguous head_dim"};
+  head_target(out, q.sizes());
+  if (out && out->scalar_type() != q.scalar_type()) throw Refused{"out must have q's dtype"};
   const at::Tensor y = out ? *out : empty(q.sizes(), q.scalar_type(), q);
   const bool with_lse = whole(a[7]) != 0;
   std::optional<at::Tensor> lse;
@@ -418,8 +427,8 @@ PyObject* paged_attention(PyObject* const* a, Py_ssize_t n) {
     if (!ws.is_contiguous()) throw Refused{"workspace must be contiguous"};
     settle(f_attention(cache, (int)m, (int)heads, q.data_ptr(), q.stride(0), q.stride(1), static_cast<const int32_t*>(table.data_ptr()),
                        table.size(1), static_cast<const int32_t*>(lens.data_ptr()),
-                       a[5] == Py_None ? 1.0f / std::sqrt((float)hd) : (float)real(a[5]), (int)std::clamp<int64_t>(whole(a[6]), -1, 0x7fffffff), y.data_ptr(), y.stride(0),
-                       y.stride(1), static_cast<float*>(ptr(lse)), ws.data_ptr(), ws.nbytes(), stream_of(dev.index)),
+                       a[5] == Py_None ? 1.0f / std::sqrt((float)hd) : (float)real(a[5]),
+                       (int)std::clamp<int64_t>(whole(a[6]), -1, 0x7fffffff), y.data_ptr(), y.stride(0), y.stride(1), static_cast<float*>(ptr(lse)), ws.data_ptr(), ws.nbytes(), stream_of(dev.index)),
            "harp_paged_attention");
   }
   return with_lse ? tuple2(y, *lse) : wrap(y);

@@ -867,3 +867,23 @@ def test_paged_attention_windows_of_any_size(rb):
         with pytest.raises(rb.HarpError):
             rb.harp_paged_attention(q, cache, table, n, window=window)
     clean(rb)
+
+
+def test_outputs_that_cannot_hold_the_result_are_refused(rb):
+    q, cache, table, n = attention_case(rb, [100, 50], 4, 2, 64, 16, torch.bfloat16)
+    over = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda").expand(2, 4, 64)
+    rope, pos = rb.HarpRope(64), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for call in (lambda: rb.harp_paged_attention(q, cache, table, n, out=over), lambda: rope(q, pos, out=over),
+                 lambda: rope.append(cache, q, q[:, :2], q[:, :2], pos, table, out=over),
+                 lambda: rb.harp_paged_attention(q, cache, table, n, out=torch.empty_like(q, dtype=torch.float32)),
+                 lambda: rope(q, pos, out=q.new_empty(2, 64, 4).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            call()
+    ol, layers, S = stack_case(rb, 256, 768, 4, 2, 64, 2, 256)
+    two = rb.HarpCache.empty(2, 8, 2, 16, 64)
+    x = torch.zeros(2, 256, device="cuda")
+    for out in (torch.empty(1, 256, device="cuda"), torch.empty(256, 2, device="cuda").t(), torch.empty(4, 128, device="cuda")):
+        with pytest.raises(ValueError):
+            S.step_cached(x, rope, two, pos, table[:, :4].contiguous(), out=out)
+    clean(rb)
+    S.close()
