@@ -473,7 +473,8 @@ harp_status harp_rope_append(harp_rope rope, const harp_kv_cache* cache, int64_t
  * Query head h reads key head h / (n_heads / n_kv_heads). A sequence of length 0 gets zeros
  * and lse -infinity; rows of negative length are left as they were; a length beyond
  * max_pages * page_size is cut to it and reported. What cache rows outside the mask hold (NaN
- * included) has no effect.
+ * included) has no effect; inside it, a value that is not finite makes its coordinate of the
+ * output not finite (NaN, also where the formula has an infinity).
  *   q, out : device [n_seqs][n_heads][head_dim] of the cache's dtype, rows on 4-byte boundaries.
  *   lse    : device fp32 [n_seqs][n_heads], log sum exp of the scaled scores, or NULL.
  *   n_seqs <= 65535; head_dim 32, 64, 96, 128, 192 or 256 (else HARP_ERR_UNSUPPORTED).

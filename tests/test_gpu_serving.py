@@ -869,6 +869,19 @@ def test_paged_attention_windows_of_any_size(rb):
     clean(rb)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_paged_attention_scales_of_any_sign(rb, scale):
+    lens = [300, 17, 0, 64]
+    q, cache, table, n = attention_case(rb, lens, 8, 2, 128, 16, torch.bfloat16)
+    out, lse = rb.harp_paged_attention(q, cache, table, n, scale=scale, return_lse=True)
+    want, wlse, mag, reach = attention64(q, cache, table, lens, scale)
+    tol, ltol = attention_tol(want, wlse, mag, reach, 128, torch.bfloat16, max(lens))
+    live = [0, 1, 3]
+    close(out, want, tol)
+    close(lse[live], wlse[live], ltol[live])
+    clean(rb)
+
+
 def test_outputs_that_cannot_hold_the_result_are_refused(rb):
     q, cache, table, n = attention_case(rb, [100, 50], 4, 2, 64, 16, torch.bfloat16)
     over = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda").expand(2, 4, 64)
