@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<HD, W>::kCtasPerSm) attention_ke
   if (lane < ST) mbar_init(&full[lane], 1);
   fence_mbar_init();
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();  // a warp's barriers are its own
   grid_wait();
   grid_release();  // join_kernel finds its pairs meanwhile
 
