@@ -38,9 +38,9 @@ constexpr int kBM = 128;        // weight rows of a tile
 constexpr int kBK = 128;        // columns of a K step = columns that share a scale
 constexpr int kSumWarps = 8;
 constexpr int kThreads = 64 + 32 * kSumWarps;
-constexpr int kMaxStages = 12;
-constexpr int kMaxAcc = 8;
-constexpr int kMaxSlots = 32;
+constexpr int kMaxStages = 12;  // of a ring
+constexpr int kMaxAcc = 4;      // accumulators in tensor memory
+constexpr int kMaxSlots = 16;   // token scales in shared memory
 
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -162,10 +162,10 @@ struct Params {
 template <int BT>
 struct Cfg {
   static constexpr int kStage = kBM * kBK + BT * kBK;
-  static constexpr int kAcc = 4;  // <= the ring's stages
+  static constexpr int kAcc = kMaxAcc;  // <= the ring's stages
   static constexpr int kPerSm = 2;  // CTAs per SM (256 of its 512 tensor-memory columns each at most)
   // ring of token scales, one slot per K step: at least stages + accumulators (see the producer)
-  static constexpr int kSlots = 16;
+  static constexpr int kSlots = kMaxSlots;
   static constexpr int kCols = kAcc * BT;  // tensor-memory columns: a power of two, at least 32
   static constexpr int kFixed = kSlots * BT * 4 + 1024 /* barriers */ + 1024 /* alignment */;
 };
